@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/jl_api.h"
+#include "jl_host.h"
 #include "jl_kernels.cuh"
 
 namespace {
@@ -15,23 +16,13 @@ namespace {
 using jl::DecodeArgs;
 using jl::PrefillArgs;
 using jl::RotateArgs;
-
-constexpr size_t kAlign = 256;
-size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
+using jl::aligned16;
+using jl::device_sms;
+using jl::encode_fn;
+using jl::fill_theta;
+using jl::fill_turns;
+using jl::resolve_scale;
+using jl::round_up;
 
 // 4-D 16-bit map over [B, rows, H, D] (innermost first: D, H, rows, B) with a
 // {64, 1, box_rows, 1} box and 128-byte swizzle.
@@ -56,29 +47,6 @@ bool encode_f16_4d(CUtensorMap* map, const void* base, int D, int H, int64_t row
   return encode_16bit_4d(map, base, D, H, rows, B, box_rows, CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
 }
 
-int device_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
-  return n;
-}
-
-void fill_theta(double* theta, int D, double base) {
-  for (int t = 0; t < D / 2; ++t) theta[t] = std::pow(base, -2.0 * t / D);
-}
-
-// theta_t / (2 pi) as u_hi + u_lo, u_hi rounded to 22 significant bits (so that
-// n * u_hi is exact in fp64 for |n| < 2^31; see sincos_int_angle).
-void fill_turns(double* u_hi, double* u_lo, const double* theta, int D) {
-  for (int t = 0; t < D / 2; ++t) {
-    const double u = theta[t] / 6.283185307179586;
-    int e = 0;
-    const double m = std::frexp(u, &e);
-    u_hi[t] = std::ldexp(std::nearbyint(std::ldexp(m, 22)), e - 22);
-    u_lo[t] = u - u_hi[t];
-  }
-}
-
 constexpr int kMaxGridYZ = 65535;  // CUDA's limit on a grid's y and z dimensions
 
 int common_checks(int B, int L, int Hq, int Hkv, int D, int w0, int w_pretrained, double rope_base, int mode) {
@@ -92,8 +60,6 @@ int common_checks(int B, int L, int Hq, int Hkv, int D, int w0, int w_pretrained
   if (B > kMaxGridYZ || Hkv > kMaxGridYZ) return JL_ERR_UNSUPPORTED;  // grid y / z dimensions
   return JL_OK;
 }
-
-float resolve_scale(float s, int D) { return s == 0.f ? 1.0f / std::sqrt((float)D) : s; }
 
 // Upper bound of the decode split count (sizes the scratch): two CTA waves
 // over all (batch, KV head) pairs at two CTAs per SM.  The scratch is then at
