@@ -378,6 +378,145 @@ int jl_bifocal_decode_noalloc(const void* q, const void* k_cache, const void* v_
                               float* lse, int B, int L, int Hq, int Hkv, int head_dim, int w0, int w_pretrained,
                               double rope_base, float softmax_scale, int mode, int* dev_error, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged cache.  Keys and values live in pages of page_size rows that sequences
+ * share; a block table [B, max_pages] (device int32) names the page that holds
+ * positions p * page_size ... of each sequence.  None of these calls looks at
+ * an entry behind a sequence's last page.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A paged cache (read by the host during the call).  k and v: bf16 device; row
+ * `row` of page `page` of KV head `g` starts at element page * page_stride +
+ * row * row_stride + g * head_stride, its head_dim values are contiguous.  Both
+ * orders of rows and heads, and k and v pages interleaved in one buffer, are
+ * strides.  page_size: a multiple of 16, 16 to 1024.  Strides: multiples of 8
+ * (JL_ERR_ALIGNMENT), without overlap (JL_ERR_INVALID_ARG).
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t num_pages;
+  int64_t page_stride, row_stride, head_stride;
+  int page_size;
+} jl_paged_kv;
+
+/*
+ * Norms of queries and keys for each head, and the position rotation, in one
+ * pass: y = R(positions[t]) (x * rsqrt(mean(x^2) + eps) * weight) for every
+ * head row x of D values (fp32, rounded to bf16 once).
+ *   q [T, Hq, D], k [T, Hkv, D]: bf16 device, a token's heads contiguous,
+ *   tokens q_stride / k_stride elements apart (multiples of 8; views of a fused
+ *   projection need no copy).
+ *   q_weight, k_weight [D] bf16, or NULL: that side is rotated without a norm.
+ *   positions: device int32 [T].  -1 marks a padded token: its output rows are
+ *   left as they were.  Other negative values do the same and set *dev_error
+ *   to 2.
+ *   q_out [T, Hq, D], k_out [T, Hkv, D]: contiguous; q_out may be q and k_out k
+ *   where those are contiguous.
+ * Launches one kernel.
+ */
+int jl_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* q_weight,
+                    const void* k_weight, float eps, const int32_t* positions, void* q_out, void* k_out, int T,
+                    int Hq, int Hkv, int head_dim, double rope_base, int* dev_error, void* stream);
+
+/*
+ * jl_qk_norm_rope whose keys, with the values v [T, Hkv, D] (copied), go to
+ * their rows of a paged cache: token t is position positions[t] of sequence
+ * seq_ids[t] (device int32 [T]; a row of block_table [B, max_pages]).  Prompt
+ * chunks of several sequences and single decode tokens may share a call; no two
+ * tokens may name the same row.  k_out [T, Hkv, D] receives the keys as well
+ * (for a prefill over contiguous keys), or NULL.  A sequence, position or page
+ * out of range leaves that token out and sets *dev_error to 2; no other row of
+ * the cache is touched.  Launches one kernel.
+ */
+int jl_qk_norm_rope_append_paged(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
+                                 const int32_t* seq_ids, const int32_t* positions, void* q_out, void* k_out,
+                                 const jl_paged_kv* cache, const int32_t* block_table, int64_t max_pages, int T,
+                                 int B, int Hq, int Hkv, int head_dim, double rope_base, int* dev_error,
+                                 void* stream);
+
+/* Scratch bytes of the two paged decode calls on this device (any batch, any length).  0 on bad arguments. */
+size_t jl_decode_paged_workspace_bytes(int Hq, int Hkv, int head_dim);
+
+/*
+ * jl_bifocal_decode_varlen over a paged cache: sequence b's query sits at
+ * position seq_lens[b] - 1 and attends to positions 0 .. seq_lens[b] - 1.
+ *   seq_lens: device int32 [B], 0 .. max_pages * page_size.  An empty sequence
+ *   (a padded slot of the batch) gives o = 0, lse = -inf.
+ *   workspace: jl_decode_paged_workspace_bytes(...) bytes, zero-filled before the
+ *   first call and after a device error 1; every other call leaves its counters
+ *   at zero.  Calls that share a workspace must not overlap on the GPU.
+ *   A length out of range counts as 0, a page out of range is left out of the
+ *   sum, and either sets *dev_error to 2.
+ *   Hq / Hkv <= 8.  The work is shared out on the device from seq_lens, so one
+ *   captured graph serves every length.
+ * Launches one kernel.
+ */
+int jl_bifocal_decode_paged(const void* q, const jl_paged_kv* cache, const int32_t* block_table, int64_t max_pages,
+                            const int32_t* seq_lens, void* o, float* lse, int B, int Hq, int Hkv, int head_dim,
+                            int w0, int w_pretrained, double rope_base, float softmax_scale, int mode,
+                            void* workspace, size_t workspace_bytes, int* dev_error, void* stream);
+
+/*
+ * The same over selected pages: KV head g of sequence b attends to the keys of
+ * pages page_list[b, g, 0 .. page_counts[b, g] - 1] (device int32 [B, Hkv,
+ * list_stride]; logical pages, i.e. columns of block_table, in any order, each
+ * once), as far as they lie before seq_lens[b].  Positions, G and the band are
+ * the sequence's own.  A count outside [0, list_stride] counts as 0, a page
+ * outside the table is left out, and either sets *dev_error to 2.
+ */
+int jl_bifocal_decode_paged_sparse(const void* q, const jl_paged_kv* cache, const int32_t* block_table,
+                                   int64_t max_pages, const int32_t* seq_lens, const int32_t* page_list,
+                                   int64_t list_stride, const int32_t* page_counts, void* o, float* lse, int B,
+                                   int Hq, int Hkv, int head_dim, int w0, int w_pretrained, double rope_base,
+                                   float softmax_scale, int mode, void* workspace, size_t workspace_bytes,
+                                   int* dev_error, void* stream);
+
+/*
+ * Summaries of the pages that hold positions starts[b] .. seq_lens[b] - 1
+ * (device int32 [B]; the pages' earlier rows count too): the mean of a page's
+ * valid keys, each taken from its position to the page's middle one,
+ * c_p = (1/n) sum_t R(page_size / 2 - t) k_{p page_size + t}, i.e. the page's
+ * mean key as one key at position p page_size + page_size / 2.  It does not
+ * depend on G.  Summed in fp32, stored as bf16 summaries [num_pages, Hkv, D]
+ * (contiguous, indexed like the cache's pages).  starts[b] >= seq_lens[b]: none.
+ *   max_new: host bound on seq_lens[b] - starts[b]; a sequence whose new tokens
+ *   touch more pages than that many tokens can sets *dev_error to 2 and is left
+ *   out, as one with a bad length, start or page is.  cache->v is not used.
+ * Launches one kernel.
+ */
+int jl_page_summaries(const jl_paged_kv* cache, const int32_t* block_table, int64_t max_pages, const int32_t* starts,
+                      const int32_t* seq_lens, int max_new, void* summaries, int B, int Hkv, int head_dim,
+                      double rope_base, int* dev_error, void* stream);
+
+/* Scratch bytes of jl_select_pages.  0 on bad arguments. */
+size_t jl_select_pages_workspace_bytes(int B, int Hkv, int64_t max_pages);
+
+/*
+ * Pages for one sparse decode step.  With i = L - 1, L = seq_lens[b], page p is
+ * scored for KV head g as a remote pair with its summary at c = p page_size +
+ * page_size / 2: the largest <R(p_q(i) - i) q_h, R(f(c) - c) c_p> of the head's
+ * queries (products, angles and sums in fp64, rounded to fp32 once).  Kept are
+ * the first sink_pages, the pages that touch the band j >= L - w0 and the last
+ * page, and the top_k best of the others; ties go to the lowest page, a NaN
+ * score is the largest.
+ *   q [B, Hq, D]: rotated at position L - 1, as for the decode.
+ *   page_list [B, Hkv, list_stride] (written): the kept pages in ascending order,
+ *   then -1; page_counts [B, Hkv] (written).  An empty sequence keeps none.
+ *   list_stride >= min(max_pages, sink_pages + top_k + ceil(w0 / page_size) + 1).
+ *   workspace: jl_select_pages_workspace_bytes(...) bytes, contents irrelevant.
+ *   A length out of range counts as 0, a page out of range scores -inf, and
+ *   either sets *dev_error to 2.
+ * Launches two kernels (one when top_k is 0).
+ */
+int jl_select_pages(const void* q, const void* summaries, int64_t num_pages, int page_size,
+                    const int32_t* block_table, int64_t max_pages, const int32_t* seq_lens, int sink_pages, int top_k,
+                    int32_t* page_list, int64_t list_stride, int32_t* page_counts, int B, int Hq, int Hkv,
+                    int head_dim, int w0, int w_pretrained, double rope_base, int mode, void* workspace,
+                    size_t workspace_bytes, int* dev_error, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

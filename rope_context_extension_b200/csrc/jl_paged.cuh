@@ -1,0 +1,124 @@
+// Kernel argument blocks and launchers of the paged-cache operators (internal;
+// the public surface is jl_api.h).
+#pragma once
+
+#include "jl_kernels.cuh"
+
+namespace jl {
+
+// Key / value pages: row `row` of page `page` of KV head `g` starts at element
+// page * page_stride + row * row_stride + g * head_stride of k (and of v).
+struct PagedView {
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  int64_t num_pages, page_stride, row_stride, head_stride;
+  int page_size;
+};
+
+// Norms of queries and keys per head, the rotation, and optionally the append
+// to a paged cache (one launch).
+struct NormRopeArgs {
+  const __nv_bfloat16* q;   // [T, Hq, D], token stride q_stride elements
+  const __nv_bfloat16* k;   // [T, Hkv, D], token stride k_stride
+  const __nv_bfloat16* v;   // [T, Hkv, D], token stride v_stride, or null (no append)
+  int64_t q_stride, k_stride, v_stride;
+  const __nv_bfloat16* qw;  // [D] norm weights, or null: no norm of the queries
+  const __nv_bfloat16* kw;  // [D], or null: no norm of the keys
+  float eps;
+  const int* positions;     // [T]; -1: a padded token, left alone
+  const int* seq_ids;       // [T] row of the block table (append)
+  __nv_bfloat16* q_out;     // [T, Hq, D]
+  __nv_bfloat16* k_out;     // [T, Hkv, D] or null
+  PagedView pages;          // append
+  const int* block_table;   // [B, max_pages]
+  int64_t max_pages;
+  int B;
+  int T, Hq, Hkv;
+  int64_t heads_per_task;   // heads of one token that one warp handles (whole passes)
+  int tasks_per_token;
+  int* dev_error;
+  double u_hi[kMaxHalfDim], u_lo[kMaxHalfDim];
+};
+cudaError_t launch_norm_rope(NormRopeArgs& a, int D, cudaStream_t stream);
+
+// Paged decode: one new query token per sequence over the pages of its block
+// table, or over the pages that page_list names.
+struct PagedDecodeArgs {
+  const __nv_bfloat16* q;    // [B, Hq, D], rotated at position L_b - 1
+  __nv_bfloat16* o;          // [B, Hq, D]
+  float* lse;                // [B, Hq] or null
+  float* warp_parts;         // [CTAs, warps] partials of items that a warp ends but did not begin
+  float* cta_parts;          // [CTAs, 2] partials of items that a CTA shares with its neighbours
+  unsigned* counters;        // [CTAs], zero between calls
+  int* dev_error;
+  const int* seq_lens;       // [B]
+  const int* block_table;    // [B, max_pages]
+  const int* page_list;      // [B, Hkv, list_stride] logical pages, or null: every page
+  const int* page_counts;    // [B, Hkv]
+  int64_t max_pages, list_stride, num_pages;
+  int page_size;
+  int B, Hq, Hkv, r;
+  int w0, w_pretrained, qshift;
+  float scale_log2;
+  double u_hi[kMaxHalfDim], u_lo[kMaxHalfDim];
+};
+cudaError_t launch_decode_paged(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedDecodeArgs& a, int D,
+                                cudaStream_t stream);
+int decode_paged_max_ctas();
+int decode_paged_warps();
+// Floats of one partial result: r maxima, r sums, r x D outputs.
+inline __host__ __device__ int64_t decode_partial_floats(int r, int D) { return (int64_t)r * (D + 2); }
+
+// Page summaries: the mean of a page's keys, each taken to the page's middle position.
+struct PageSummaryArgs {
+  PagedView pages;
+  const int* block_table;    // [B, max_pages]
+  const int* starts;         // [B] first position whose page is summarised
+  const int* seq_lens;       // [B]
+  __nv_bfloat16* summaries;  // [num_pages, Hkv, D]
+  int64_t max_pages;
+  int B, Hkv;
+  int pages_per_seq;         // bound on the pages one sequence's new tokens touch
+  int* dev_error;
+  double u_hi[kMaxHalfDim], u_lo[kMaxHalfDim];
+};
+cudaError_t launch_page_summaries(const PageSummaryArgs& a, int D, cudaStream_t stream);
+
+// Page scores and the selection of each KV head's pages.
+struct PageSelectArgs {
+  const __nv_bfloat16* q;          // [B, Hq, D], rotated at position L_b - 1
+  const __nv_bfloat16* summaries;  // [num_pages, Hkv, D]
+  const int* block_table;          // [B, max_pages]
+  const int* seq_lens;             // [B]
+  float* scores;                   // scratch [B, Hkv, max_pages]
+  int* page_list;                  // [B, Hkv, list_stride]
+  int* page_counts;                // [B, Hkv]
+  int64_t max_pages, list_stride, num_pages;
+  int page_size;
+  int B, Hq, Hkv, r;
+  int w0, w_pretrained, qshift;
+  int sink_pages, top_k;
+  int* dev_error;
+  double u_hi[kMaxHalfDim], u_lo[kMaxHalfDim];
+};
+cudaError_t launch_page_select(const PageSelectArgs& a, int D, cudaStream_t stream);
+
+// cos and sin of n * theta (theta / 2 pi = u_hi + u_lo as sincos_int_angle takes
+// it): whole turns removed exactly in fp64, the rest in fp32.  The remainder, at
+// most half a turn, is rounded to fp32 once (2^-26 turns, 1e-7 rad), far inside
+// the bf16 rounding (2^-9) or the hi + lo split (2^-17) of what is rotated.
+__device__ __forceinline__ void sincos_turns(int64_t n, double u_hi, double u_lo, float* s, float* c) {
+  double a = (double)n * u_hi;  // exact for |n| < 2^31
+  a -= rint(a);
+  double f = a + (double)n * u_lo;
+  f -= rint(f);
+  sincospif(2.f * (float)f, s, c);
+}
+
+// A sequence's length as the paged operators take it: 0 .. max_pages * page_size,
+// anything else counts as empty (the caller flags kDevBadLength).
+__device__ __forceinline__ bool paged_length_ok(int L, int64_t max_pages, int page_size) {
+  return L >= 0 && (int64_t)L <= max_pages * page_size && L <= (1 << 30);
+}
+
+}  // namespace jl

@@ -20,6 +20,8 @@ __all__ = [
     "jl_bifocal_decode_noalloc", "jl_bifocal_decode_varlen", "jl_rope_append", "jl_prefill_chunk_workspace_bytes",
     "jl_bifocal_prefill_chunk", "jl_prefill_ie_workspace_bytes", "jl_bifocal_prefill_ie", "jl_bifocal_decode_range",
     "jl_decode_combine", "jl_wait_timeout_check", "jl_prefill_tile_classes",
+    "jl_qk_norm_rope", "jl_qk_norm_rope_append_paged", "jl_decode_paged_workspace_bytes", "jl_bifocal_decode_paged",
+    "jl_bifocal_decode_paged_sparse", "jl_page_summaries", "jl_select_pages_workspace_bytes", "jl_select_pages",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -36,12 +38,21 @@ EXPORTED_SYMBOLS = (
     "jl_prefill_attention", "jl_bifocal_decode_noalloc", "jl_bifocal_decode_varlen", "jl_rope_append",
     "jl_prefill_chunk_workspace_bytes", "jl_bifocal_prefill_chunk", "jl_prefill_ie_workspace_bytes",
     "jl_bifocal_prefill_ie", "jl_bifocal_decode_range", "jl_decode_combine",
-    "jl_wait_timeout_check", "jl_prefill_tile_classes",
+    "jl_wait_timeout_check", "jl_prefill_tile_classes", "jl_qk_norm_rope", "jl_qk_norm_rope_append_paged",
+    "jl_decode_paged_workspace_bytes", "jl_bifocal_decode_paged", "jl_bifocal_decode_paged_sparse",
+    "jl_page_summaries", "jl_select_pages_workspace_bytes", "jl_select_pages",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libjetlong.so")
 _lib = None
+
+
+class _PagedKV(ctypes.Structure):
+    """jl_paged_kv (include/jl_api.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int)]
 
 
 class JetLongError(RuntimeError):
@@ -105,6 +116,28 @@ def lib() -> ctypes.CDLL:
     L.jl_bifocal_decode_range.restype = c_i
     L.jl_decode_combine.argtypes = [c_p, c_p, c_i, c_p, c_p, c_i, c_i, c_i, c_p]
     L.jl_decode_combine.restype = c_i
+    c_kv = ctypes.POINTER(_PagedKV)
+    L.jl_qk_norm_rope.argtypes = [c_p, c_i64, c_p, c_i64, c_p, c_p, c_f, c_p, c_p, c_p, c_i, c_i, c_i, c_i, c_d, c_p,
+                                  c_p]
+    L.jl_qk_norm_rope.restype = c_i
+    L.jl_qk_norm_rope_append_paged.argtypes = [c_p, c_i64, c_p, c_i64, c_p, c_i64, c_p, c_p, c_f, c_p, c_p, c_p, c_p,
+                                               c_kv, c_p, c_i64, c_i, c_i, c_i, c_i, c_i, c_d, c_p, c_p]
+    L.jl_qk_norm_rope_append_paged.restype = c_i
+    L.jl_decode_paged_workspace_bytes.argtypes = [c_i, c_i, c_i]
+    L.jl_decode_paged_workspace_bytes.restype = c_sz
+    L.jl_bifocal_decode_paged.argtypes = [c_p, c_kv, c_p, c_i64, c_p, c_p, c_p, c_i, c_i, c_i, c_i, c_i, c_i, c_d,
+                                          c_f, c_i, c_p, c_sz, c_p, c_p]
+    L.jl_bifocal_decode_paged.restype = c_i
+    L.jl_bifocal_decode_paged_sparse.argtypes = [c_p, c_kv, c_p, c_i64, c_p, c_p, c_i64, c_p, c_p, c_p, c_i, c_i,
+                                                 c_i, c_i, c_i, c_i, c_d, c_f, c_i, c_p, c_sz, c_p, c_p]
+    L.jl_bifocal_decode_paged_sparse.restype = c_i
+    L.jl_page_summaries.argtypes = [c_kv, c_p, c_i64, c_p, c_p, c_i, c_p, c_i, c_i, c_i, c_d, c_p, c_p]
+    L.jl_page_summaries.restype = c_i
+    L.jl_select_pages_workspace_bytes.argtypes = [c_i, c_i, c_i64]
+    L.jl_select_pages_workspace_bytes.restype = c_sz
+    L.jl_select_pages.argtypes = [c_p, c_p, c_i64, c_i, c_p, c_i64, c_p, c_i, c_i, c_p, c_i64, c_p, c_i, c_i, c_i,
+                                  c_i, c_i, c_i, c_d, c_i, c_p, c_sz, c_p, c_p]
+    L.jl_select_pages.restype = c_i
     L.jl_wait_timeout_check.argtypes = [c_p, c_d, c_p]
     L.jl_wait_timeout_check.restype = c_i
     _lib = L
@@ -409,3 +442,237 @@ def jl_wait_timeout_check(dev_error, timeout_s: float = 0.2, stream=None):
     import torch
     _check_tensor(dev_error, "dev_error", torch.int32)
     _check(lib().jl_wait_timeout_check(_ptr(dev_error), float(timeout_s), _stream(stream)), "jl_wait_timeout_check")
+
+
+# ---------------------------------------------------------------------------
+# Paged cache.  k_pages / v_pages are [num_pages, page_size, Hkv, D] tensors of
+# any strides whose rows are contiguous and do not overlap (a permuted
+# [num_pages, Hkv, page_size, D] pool, or the two halves of one pool); every
+# tensor of a call lives on the same device, which need not be the current one.
+# ---------------------------------------------------------------------------
+def _check_on(dev, specs):
+    """specs: (tensor, name, dtype, shape or None) of contiguous tensors on device dev."""
+    for t, name, dtype, shape in specs:
+        _check_tensor(t, name, dtype, shape)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{dev}")
+
+
+def _check_opt(dev, t, name, dtype, shape):
+    if t is not None:
+        _check_on(dev, ((t, name, dtype, shape),))
+
+
+def _head_rows(t, name, T, H, D, dev):
+    """Token stride of a [T, H, D] bf16 view whose heads are contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != (T, H, D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H, D)}")
+    st = t.stride()
+    if st[2] != 1 or (H > 1 and st[1] != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return st[0] if T > 1 else H * D
+
+
+def _paged_kv(k_pages, v_pages, dev, heads=None, head_dim=None):
+    import torch
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t is None and name == "v_pages":
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be [num_pages, page_size, Hkv, D] with contiguous rows")
+    n, P, H, D = k_pages.shape
+    if heads is not None and (H, D) != (heads, head_dim):
+        raise ValueError(f"k_pages holds {H} heads of {D}, expected {heads} of {head_dim}")
+    sp, sr, sh, _ = k_pages.stride()
+    if v_pages is not None and (v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride()):
+        raise ValueError("k_pages and v_pages must have the same shape and strides")
+    if H == 1:  # a dimension of one has no stride of its own
+        sh = D
+    if n == 1:
+        sp = (P - 1) * sr + (H - 1) * sh + D
+        sp += -sp % 8
+    return _PagedKV(k_pages.data_ptr(), 0 if v_pages is None else v_pages.data_ptr(), n, sp, sr, sh, P)
+
+
+def _on_device(dev):
+    """A context with device dev current (none needed when it is already)."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+
+
+def _workspace(dev, workspace):
+    if workspace is None:
+        return 0
+    if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
+    return workspace.numel() * workspace.element_size()
+
+
+def jl_qk_norm_rope(q, k, q_weight, k_weight, positions, q_out, k_out, *, eps: float, rope_base: float,
+                    dev_error=None, stream=None):
+    """Per-head norm of queries and keys and their rotation in one pass.  q [T, Hq, D] and
+    k [T, Hkv, D] (bf16, CUDA; views of a fused projection are fine), weights [D] bf16 or None
+    (no norm on that side), positions int32 [T] (-1: padded token, left alone), q_out / k_out
+    contiguous (they may be q / k)."""
+    import torch
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    dev = q.get_device()
+    qs, ks = _head_rows(q, "q", T, Hq, D, dev), _head_rows(k, "k", T, Hkv, D, dev)
+    bf16, i32 = torch.bfloat16, torch.int32
+    _check_on(dev, ((positions, "positions", i32, (T,)), (q_out, "q_out", bf16, (T, Hq, D)),
+                    (k_out, "k_out", bf16, (T, Hkv, D))))
+    _check_opt(dev, q_weight, "q_weight", bf16, (D,))
+    _check_opt(dev, k_weight, "k_weight", bf16, (D,))
+    _check_opt(dev, dev_error, "dev_error", i32, None)
+    with _on_device(dev):
+        st = lib().jl_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), float(eps),
+                                   _ptr(positions), _ptr(q_out), _ptr(k_out), T, Hq, Hkv, D, float(rope_base),
+                                   _ptr(dev_error), _stream(stream))
+    _check(st, "jl_qk_norm_rope")
+
+
+def jl_qk_norm_rope_append_paged(q, k, v, q_weight, k_weight, seq_ids, positions, block_table, q_out, k_pages,
+                                 v_pages, *, eps: float, rope_base: float, k_out=None, dev_error=None, stream=None):
+    """jl_qk_norm_rope whose keys, and the values v [T, Hkv, D], go to row positions[t] of
+    sequence seq_ids[t] (int32 [T], a row of block_table int32 [B, max_pages]) of the paged
+    cache; k_out [T, Hkv, D] (or None) receives the keys too."""
+    import torch
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    dev = q.get_device()
+    qs, ks = _head_rows(q, "q", T, Hq, D, dev), _head_rows(k, "k", T, Hkv, D, dev)
+    vs = _head_rows(v, "v", T, Hkv, D, dev)
+    bf16, i32 = torch.bfloat16, torch.int32
+    B, M = block_table.shape
+    _check_on(dev, ((seq_ids, "seq_ids", i32, (T,)), (positions, "positions", i32, (T,)),
+                    (block_table, "block_table", i32, (B, M)), (q_out, "q_out", bf16, (T, Hq, D))))
+    _check_opt(dev, k_out, "k_out", bf16, (T, Hkv, D))
+    _check_opt(dev, q_weight, "q_weight", bf16, (D,))
+    _check_opt(dev, k_weight, "k_weight", bf16, (D,))
+    _check_opt(dev, dev_error, "dev_error", i32, None)
+    kv = _paged_kv(k_pages, v_pages, dev, Hkv, D)
+    with _on_device(dev):
+        st = lib().jl_qk_norm_rope_append_paged(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight),
+                                                _ptr(k_weight), float(eps), _ptr(seq_ids), _ptr(positions),
+                                                _ptr(q_out), _ptr(k_out), ctypes.byref(kv), _ptr(block_table), M, T,
+                                                B, Hq, Hkv, D, float(rope_base), _ptr(dev_error), _stream(stream))
+    _check(st, "jl_qk_norm_rope_append_paged")
+
+
+def jl_decode_paged_workspace_bytes(Hq: int, Hkv: int, head_dim: int) -> int:
+    return int(lib().jl_decode_paged_workspace_bytes(Hq, Hkv, head_dim))
+
+
+def _decode_paged_tensors(q, k_pages, v_pages, block_table, seq_lens, o, lse, workspace, dev_error):
+    import torch
+    B, Hq, D = q.shape
+    dev = q.get_device()
+    bf16, i32 = torch.bfloat16, torch.int32
+    M = block_table.shape[1]
+    _check_on(dev, ((q, "q", bf16, None), (block_table, "block_table", i32, (B, M)),
+                    (seq_lens, "seq_lens", i32, (B,)), (o, "o", bf16, (B, Hq, D))))
+    _check_opt(dev, lse, "lse", torch.float32, (B, Hq))
+    _check_opt(dev, dev_error, "dev_error", i32, None)
+    kv = _paged_kv(k_pages, v_pages, dev)
+    if k_pages.shape[3] != D:
+        raise ValueError(f"k_pages holds rows of {k_pages.shape[3]}, expected {D}")
+    return B, Hq, k_pages.shape[2], D, M, dev, kv, _workspace(dev, workspace)
+
+
+def jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seq_lens, o, lse, *, w0: int, w_pretrained: int,
+                            rope_base: float, softmax_scale: float = 0.0, mode: int = JL_QSHIFT_SELF_EXTEND,
+                            workspace=None, dev_error=None, stream=None):
+    """Decode over a paged cache: block_table int32 [B, max_pages], seq_lens int32 [B] (0: a
+    padded slot, o = 0 and lse = -inf); q / o [B, Hq, D]; lse [B, Hq] fp32 or None; workspace:
+    zero-initialised uint8 CUDA tensor of jl_decode_paged_workspace_bytes(...) bytes."""
+    B, Hq, Hkv, D, M, dev, kv, ws_bytes = _decode_paged_tensors(q, k_pages, v_pages, block_table, seq_lens, o, lse,
+                                                                workspace, dev_error)
+    with _on_device(dev):
+        st = lib().jl_bifocal_decode_paged(_ptr(q), ctypes.byref(kv), _ptr(block_table), M, _ptr(seq_lens), _ptr(o),
+                                           _ptr(lse), B, Hq, Hkv, D, int(w0), int(w_pretrained), float(rope_base),
+                                           float(softmax_scale), int(mode), _ptr(workspace), ws_bytes,
+                                           _ptr(dev_error), _stream(stream))
+    _check(st, "jl_bifocal_decode_paged")
+
+
+def jl_bifocal_decode_paged_sparse(q, k_pages, v_pages, block_table, seq_lens, page_list, page_counts, o, lse, *,
+                                   w0: int, w_pretrained: int, rope_base: float, softmax_scale: float = 0.0,
+                                   mode: int = JL_QSHIFT_SELF_EXTEND, workspace=None, dev_error=None, stream=None):
+    """jl_bifocal_decode_paged over the pages that page_list int32 [B, Hkv, n] names (logical
+    pages, the first page_counts[b, g] of each row; page_counts int32 [B, Hkv])."""
+    import torch
+    B, Hq, Hkv, D, M, dev, kv, ws_bytes = _decode_paged_tensors(q, k_pages, v_pages, block_table, seq_lens, o, lse,
+                                                                workspace, dev_error)
+    n = page_list.shape[2]
+    _check_on(dev, ((page_list, "page_list", torch.int32, (B, Hkv, n)),
+                    (page_counts, "page_counts", torch.int32, (B, Hkv))))
+    with _on_device(dev):
+        st = lib().jl_bifocal_decode_paged_sparse(_ptr(q), ctypes.byref(kv), _ptr(block_table), M, _ptr(seq_lens),
+                                                  _ptr(page_list), n, _ptr(page_counts), _ptr(o), _ptr(lse), B, Hq,
+                                                  Hkv, D, int(w0), int(w_pretrained), float(rope_base),
+                                                  float(softmax_scale), int(mode), _ptr(workspace), ws_bytes,
+                                                  _ptr(dev_error), _stream(stream))
+    _check(st, "jl_bifocal_decode_paged_sparse")
+
+
+def jl_page_summaries(k_pages, block_table, starts, seq_lens, summaries, *, max_new: int, rope_base: float,
+                      dev_error=None, stream=None):
+    """Mean key of every page that holds positions starts[b] .. seq_lens[b] - 1 (int32 [B]) into
+    summaries [num_pages, Hkv, D] (bf16, contiguous, indexed like the pages); max_new >= every
+    seq_lens[b] - starts[b]."""
+    import torch
+    B, M = block_table.shape
+    dev = k_pages.get_device()
+    n, _, Hkv, D = k_pages.shape
+    i32 = torch.int32
+    _check_on(dev, ((block_table, "block_table", i32, (B, M)), (starts, "starts", i32, (B,)),
+                    (seq_lens, "seq_lens", i32, (B,)), (summaries, "summaries", torch.bfloat16, (n, Hkv, D))))
+    _check_opt(dev, dev_error, "dev_error", i32, None)
+    kv = _paged_kv(k_pages, None, dev)
+    with _on_device(dev):
+        st = lib().jl_page_summaries(ctypes.byref(kv), _ptr(block_table), M, _ptr(starts), _ptr(seq_lens),
+                                     int(max_new), _ptr(summaries), B, Hkv, D, float(rope_base), _ptr(dev_error),
+                                     _stream(stream))
+    _check(st, "jl_page_summaries")
+
+
+def jl_select_pages_workspace_bytes(B: int, Hkv: int, max_pages: int) -> int:
+    return int(lib().jl_select_pages_workspace_bytes(B, Hkv, max_pages))
+
+
+def jl_select_pages(q, summaries, block_table, seq_lens, page_list, page_counts, *, page_size: int, sink_pages: int,
+                    top_k: int, w0: int, w_pretrained: int, rope_base: float, mode: int = JL_QSHIFT_SELF_EXTEND,
+                    workspace=None, dev_error=None, stream=None):
+    """Pages for a sparse decode step: the first sink_pages, those of the band and the top_k
+    best by score, per KV head, ascending into page_list int32 [B, Hkv, n] (-1 behind them) and
+    page_counts int32 [B, Hkv].  n >= min(max_pages, sink_pages + top_k + ceil(w0 / page_size) + 1);
+    workspace: uint8 CUDA tensor of jl_select_pages_workspace_bytes(...) bytes."""
+    import torch
+    B, Hq, D = q.shape
+    num_pages, Hkv, _ = summaries.shape
+    M = block_table.shape[1]
+    n = page_list.shape[2]
+    dev = q.get_device()
+    bf16, i32 = torch.bfloat16, torch.int32
+    _check_on(dev, ((q, "q", bf16, None), (summaries, "summaries", bf16, (num_pages, Hkv, D)),
+                    (block_table, "block_table", i32, (B, M)), (seq_lens, "seq_lens", i32, (B,)),
+                    (page_list, "page_list", i32, (B, Hkv, n)), (page_counts, "page_counts", i32, (B, Hkv))))
+    _check_opt(dev, dev_error, "dev_error", i32, None)
+    ws_bytes = _workspace(dev, workspace)
+    with _on_device(dev):
+        st = lib().jl_select_pages(_ptr(q), _ptr(summaries), num_pages, int(page_size), _ptr(block_table), M,
+                                   _ptr(seq_lens), int(sink_pages), int(top_k), _ptr(page_list), n,
+                                   _ptr(page_counts), B, Hq, Hkv, D, int(w0), int(w_pretrained), float(rope_base),
+                                   int(mode), _ptr(workspace), ws_bytes, _ptr(dev_error), _stream(stream))
+    _check(st, "jl_select_pages")
