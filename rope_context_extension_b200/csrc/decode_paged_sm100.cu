@@ -26,15 +26,16 @@
 // ticket (no spinning), each time in unit order, so results do not depend on
 // timing.
 //
-// Scores use mma.sync m16n8k16 with the query heads on the M axis.  A remote
-// unit starting at position j0 has dk(j) = dk(j0) - e(j) with e(j) in [0, 15]:
-// the query takes R(dq - dk(j0)) (its D/2 factors formed by the warp's lanes for
-// each unit) and the keys R(-e) from a 16-row table, in registers.  Corrected
+// Scores use mma.sync m16n8k16 with the query heads on the M axis.  A remote unit
+// that starts at position j0 has dk(j) = dk(j0) - e(j) with e(j) in [0, 15]: the
+// queries take R(dq - dk(j0)), whose D/2 factors the warp's lanes form once per
+// unit, and the keys take R(-e) from a 16-row table, in registers.  Corrected
 // operands enter the products as bf16 hi + lo pairs (about 16 significant bits;
-// one bf16 would put 2^-9 |q| |k| on a score), the query's lo part in the M rows
-// 8-15 that at most 8 heads leave free.  Probabilities are carried as hi + lo
-// pairs too, so that the output's error is its own rounding; for up to four
-// heads the lo parts use the columns 4-7 of the P V product that would be idle.
+// one bf16 would put 2^-9 |q| |k| on a score), the queries' lo parts in the M rows
+// 8-15 that at most eight heads leave free.  Probabilities are carried as hi + lo
+// pairs too (2^-17; one bf16 would double the output's own rounding error): for up
+// to four heads, duplicated in M rows 4-7, the lo parts use the columns 4-7 of the
+// P V product, which would be idle.
 #include "jl_mma.cuh"
 #include "jl_paged.cuh"
 
@@ -42,30 +43,46 @@ namespace jl {
 
 namespace {
 
-constexpr int kWarps = 12;
+constexpr int kSegs = 128;  // runs of items whose unit counts the CTA scans
+
+#ifndef JL_PG_WARPS
+#define JL_PG_WARPS 12
+#endif
+#ifndef JL_PG_SLOTS
+#define JL_PG_SLOTS 3
+#endif
+constexpr int kWarps = JL_PG_WARPS;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMinUnits = 2 * kWarps;  // units per CTA below which fewer CTAs share a call's work
+constexpr int kMaxR = 8;
 
 template <int D>
 struct PgCfg {
-  static constexpr int kChunks = D / 64;
-  static constexpr int kHalf = 16 * D * 2;         // bytes of a unit's keys (or values)
-  static constexpr int kSlot = 2 * kHalf;
-  static constexpr int kSlots = D == 128 ? 2 : 4;  // ring depth of a warp
-  static constexpr int kERow = (D / 2 + 8) * 8;    // bytes per row of the key factors (padded)
+  static constexpr int kSlot = 16 * D * 2;         // bytes of a unit's keys, or of its values
+  static constexpr int kSlots = JL_PG_SLOTS * (128 / D);  // ring depth of a warp: keys, values, keys, ...
+  static constexpr int kMeta = 4;                  // units described ahead (a power of two)
   static constexpr int kRing = kWarps * kSlots * kSlot;
-  static constexpr int kEOff = kRing;
-  static constexpr int kUOff = kEOff + 16 * kERow;           // [D/2] (u_hi, u_lo)
-  static constexpr int kCsOff = kUOff + (D / 2) * 16;        // [warps][D/2] query factors
-  static constexpr int kScanOff = kCsOff + kWarps * (D / 2) * 8;  // [threads + 1] running unit counts
-  static constexpr int kBarOff = kScanOff + (kThreads + 1) * 8 + 8;
-  static constexpr int kMiscOff = kBarOff + kWarps * kSlots * 8;
-  static constexpr int kSmem = kMiscOff + 256 + 1024;
+  static constexpr int kERow = D * 4 + 64;         // bytes per row of the key factors (padded)
+  static constexpr int kERows = 32;
+  static constexpr int kEOff = kRing;              // key factors [32][D/4] x (c, c, s, s)
+  static constexpr int kCsOff = kEOff + kERows * kERow;  // a warp's query factors [D/4] x (c, c, s, s)
+  static constexpr int kQOff = kCsOff + kWarps * D * 4;  // a warp's turned query fragments
+  static constexpr int kQBytes = D * 32;
+  static constexpr int kScanOff = kQOff + kWarps * kQBytes;  // running unit counts
+  static constexpr int kBarOff = kScanOff + (kSegs + 1) * 8 + 8;
+  static constexpr int kMetaOff = (kBarOff + kWarps * kSlots * 8 + 15) / 16 * 16;  // units: item, position, index
+  static constexpr int kMiscOff = kMetaOff + kWarps * kMeta * 16;
+  static constexpr int kEntOff = kMiscOff + 16;    // the warps' partials: items, first units, sizes
+  static constexpr int kSmem = kEntOff + 32 * kWarps + 1024;
+  static constexpr int kWtsOff = kQOff;            // the joins' weights; the query fragments are done with
+  static constexpr int kMaxParts = 256;            // parts that one join weighs: CTAs of a device, warps of a CTA
+  static_assert((kMaxR * kMaxParts + 2 * kMaxR) * 4 <= kWarps * kQBytes, "room for the weights");
+  static_assert(kSmem <= 232448, "shared memory");
 };
 
 // Units of item it = b * Hkv + g.
-__device__ __forceinline__ int item_units(const PagedDecodeArgs& a, int64_t it) {
-  const int b = (int)(it / a.Hkv);
+__device__ __forceinline__ int item_units(const PagedDecodeArgs& a, int it) {
+  const int b = it / a.Hkv;
   const int L = a.seq_lens[b];
   if (!paged_length_ok(L, a.max_pages, a.page_size)) return 0;
   if (a.page_list == nullptr) return (L + 15) >> 4;
@@ -74,15 +91,53 @@ __device__ __forceinline__ int item_units(const PagedDecodeArgs& a, int64_t it) 
   return n * (a.page_size >> 4);
 }
 
+// One 16-row box of a page: coordinates (0, row, 0, head, page) of the 5-D map
+// (64 dims, rows, D/64, heads, pages), so the tile lands as D/64 blocks of 16 x 128 bytes.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row, int head,
+                                            int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %2, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void lds_f4(uint32_t addr, float4& f) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(addr));
+}
+
+__device__ __forceinline__ void lds_u4(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
+}
+
+// B fragments of k-step ks for the unit's 16 keys; tile: the lane's place in the unit's keys.
+template <int D>
+__device__ __forceinline__ void load_keys(uint32_t tile, int ks, uint32_t (&k)[4]) {
+  ldsm_x4((tile ^ ((ks & 3) << 5)) + (ks >> 2) * 2048, k[0], k[1], k[2], k[3]);
+}
+
 // Scratch partial: [r] maxima (log2 units), [r] sums, [r][D] outputs.
 struct Partial {
   float* m;
   float* l;
   float* o;
 };
-__device__ __forceinline__ Partial partial_at(float* base, int64_t idx, int r, int D) {
-  float* p = base + idx * decode_partial_floats(r, D);
+__device__ __forceinline__ Partial partial_at(float* base, int64_t idx, int r, int D, int64_t stride = 0) {
+  float* p = base + idx * (stride ? stride : decode_partial_floats(r, D));
   return {p, p + r, p + 2 * r};
+}
+
+// cos and sin of n turns' worth of theta: turn = theta / 2 pi in 64-bit fixed
+// point, whole turns fall off the top.  The phase is good to 2^-31 turns plus
+// n 2^-56, the MUFU's sine and cosine to 2^-21 (their documented bound in
+// [-pi, pi]), which puts 2^-21 |q| |k| on a score.
+__device__ __forceinline__ void sincos_phase(int n, uint64_t turn, float* s, float* c) {
+  const uint32_t m = (uint32_t)(n < 0 ? -n : n);
+  const uint32_t ph = m * (uint32_t)(turn >> 32) + __umulhi(m, (uint32_t)turn);
+  const float x = (float)(int32_t)ph * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float sn = __sinf(x);
+  *s = n < 0 ? -sn : sn;
+  *c = __cosf(x);
 }
 
 // kPack: at most four query heads per KV head, duplicated in M rows 4-7 so that
@@ -92,7 +147,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ PagedDecodeArgs a) {
   using C = PgCfg<D>;
-  constexpr int H2 = D / 2;
   constexpr int KS = D / 16;   // k-steps of the score product
   constexpr int KS2 = D / 32;  // k-steps holding the first half of each pair
   constexpr int S = C::kSlots;
@@ -101,51 +155,75 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = a.r;
-  const int64_t items = (int64_t)a.B * a.Hkv;
+  const int items = a.B * a.Hkv;
+
+  const int c4 = lane & 3, hrow = lane >> 2;  // column group and row of the mma fragments
+  const int hq = kPack ? (hrow & 3) : hrow;   // query head of that row
+  const int qt = D == 128 ? 2 * lane : 2 * (lane & 15);  // the pairs qt, qt + 1 whose factors this lane forms
+  // theta / 2 pi of those pairs, read once through a generic pointer (an indexed
+  // parameter read serialises over the lanes)
+  uint64_t turn0, turn1;
+  {
+    const uint64_t* tp = a.turn;
+    asm volatile("" : "+l"(tp));
+    turn0 = tp[qt];
+    turn1 = tp[qt + 1];
+  }
 
   int64_t* scan = reinterpret_cast<int64_t*>(smem + C::kScanOff);
   volatile int* misc = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
   volatile int* abort_flag = misc;               // [0]
-  volatile int* ticket = misc + 1;               // [1], [2]
-  volatile int* ent_item = misc + 4;             // [2 x warps] items of the partials, -1: none
-  double2* utab = reinterpret_cast<double2*>(smem + C::kUOff);
+  volatile int* ticket = misc + 1;               // [1]
+  struct Entry {
+    int64_t s;  // the item's first unit
+    int n;      // its units
+    int item;   // -1: no partial
+  };
+  Entry* ent = reinterpret_cast<Entry*>(smem + C::kEntOff);  // the warps' heads (2 w) and tails (2 w + 1)
 
+  bool any_empty;
   // ---- how much there is to do, and where this CTA's and this warp's share is
-  const int64_t per_thread = (items + kThreads - 1) / kThreads;
-  int64_t mine = 0;
-  for (int64_t i = tid * per_thread; i < min(items, (tid + 1) * per_thread); ++i) mine += item_units(a, i);
+  const int per_seg = (items + kSegs - 1) / kSegs;
+  if (tid < kWarps * S) mbar_init(smem_addr(smem + C::kBarOff) + 8 * tid, 1);
+  if (tid == 0) {
+    fence_mbar_init();
+    *abort_flag = 0;
+    scan[0] = 0;
+  }
+  if (tid < 2 * kWarps) ent[tid].item = -1;
   {
-    int64_t v = mine;
+    int64_t v = 0;
+    bool none = false;
+    if (tid < kSegs) {
+      for (int i = tid * per_seg; i < items && i < (tid + 1) * per_seg; ++i) {
+        const int n = item_units(a, i);
+        none = none || n == 0;
+        v += n;
+      }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += t;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+      }
+      scan[tid + 1] = v;
     }
-    scan[tid + 1] = v;
-    if (tid == 0) {
-      scan[0] = 0;
-      *abort_flag = 0;
-    }
-    if (tid < kWarps * S) mbar_init(smem_addr(smem + C::kBarOff) + 8 * tid, 1);
-    if (tid == 0) fence_mbar_init();
-    if (tid < 2 * kWarps) ent_item[tid] = -1;
-    if (tid < H2) utab[tid] = make_double2(a.u_hi[tid], a.u_lo[tid]);
-    __syncthreads();
+    any_empty = __syncthreads_or(none);
     int64_t before = 0;
-    for (int w = 0; w < warp; ++w) before += scan[32 * w + 32];
+    if (tid < kSegs)
+      for (int w = 0; w < warp; ++w) before += scan[32 * w + 32];
     __syncthreads();
-    scan[tid + 1] = v + before;
+    if (tid < kSegs) scan[tid + 1] = v + before;
     __syncthreads();
   }
-  const int64_t U = scan[kThreads];
+  const int64_t U = scan[kSegs];
 
   // Sequences and lists with nothing in them, bad lengths and counts: spread over every CTA.
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+  for (int it = any_empty ? blockIdx.x : items; it < items; it += gridDim.x) {
     if (item_units(a, it) != 0) continue;
-    const int b = (int)(it / a.Hkv);
-    for (int i = tid; i < r * D; i += kThreads)
-      a.o[((int64_t)b * a.Hq + (it - (int64_t)b * a.Hkv) * r) * D + i] = __float2bfloat16_rn(0.f);
-    if (a.lse != nullptr && tid < r) a.lse[(int64_t)b * a.Hq + (it - (int64_t)b * a.Hkv) * r + tid] = -INFINITY;
+    const int b = it / a.Hkv;
+    const int64_t row = (int64_t)b * a.Hq + (it - b * a.Hkv) * r;
+    for (int i = tid; i < r * D; i += kThreads) a.o[row * D + i] = __float2bfloat16_rn(0.f);
+    if (a.lse != nullptr && tid < r) a.lse[row + tid] = -INFINITY;
     if (tid == 0 && a.dev_error) {
       bool bad = !paged_length_ok(a.seq_lens[b], a.max_pages, a.page_size);
       if (a.page_list != nullptr) bad = bad || a.page_counts[it] < 0 || a.page_counts[it] > a.list_stride;
@@ -160,38 +238,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t wb = c0 + warp * (c1 - c0) / kWarps, we = c0 + (warp + 1) * (c1 - c0) / kWarps;
   const int cnt = (int)(we - wb);
 
-  // Key factors E[e][t] = R(-e) for e < 16, as (c_t, c_t+1, s_t, s_t+1) for even t.
-  for (int idx = tid; idx < 16 * H2; idx += kThreads) {
-    const int e = idx / H2, t = idx % H2;
-    float sn, cs;
-    sincos_turns(-e, utab[t].x, utab[t].y, &sn, &cs);
-    float* dst = reinterpret_cast<float*>(smem + C::kEOff) + e * (C::kERow / 4);
-    dst[(t >> 1) * 4 + (t & 1)] = cs;
-    dst[(t >> 1) * 4 + 2 + (t & 1)] = sn;
-  }
-
   // ---- the walk over units: lane l holds the description of unit 32 * batch + l
-  int64_t cur_it = 0, cur_s = 0;  // an item at or before the batch's first unit, and its first unit
+  int cur_it = 0;
+  int64_t cur_s = 0;  // cur_it: an item at or before the batch's first unit; cur_s: its first unit
   if (cnt > 0) {
-    // the thread segment of items that holds unit wb, found by all lanes together
+    // the run of items that holds unit wb, found by all lanes together
     int seg = 0;
-    for (int t0 = 0; t0 < kThreads; t0 += 32) {
+    for (int t0 = 0; t0 < kSegs; t0 += 32) {
       const unsigned below = __ballot_sync(0xffffffffu, scan[t0 + lane] <= wb);
       if (below == 0u) break;
       seg = t0 + 31 - __clz(below);
       if (below != 0xffffffffu) break;
     }
-    cur_it = seg * per_thread;
+    cur_it = seg * per_seg;
     cur_s = scan[seg];
   }
-  int m_item = 0, m_phys = -1, m_row = 0, m_j0 = 0, m_c = 0;
+  int m_item = 0, m_g = 0, m_phys = -1, m_row = 0, m_j0 = 0, m_c = 0;
   auto load_batch = [&](int k0) {
     const int64_t x = wb + k0 + lane;
     const bool valid = k0 + lane < cnt;
-    int64_t my_it = -1, my_s = 0;
+    int my_it = -1;
+    int64_t my_s = 0;
     bool open = valid;
     while (__any_sync(0xffffffffu, open)) {
-      const int64_t i = cur_it + lane;
+      const int i = cur_it + lane;
       int n = i < items ? item_units(a, i) : 0;
       int64_t p = n;
 #pragma unroll
@@ -224,18 +294,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     m_j0 = -1;
     m_row = 0;
     m_c = 0;
-    m_item = (int)my_it;
+    m_item = my_it;
     if (valid && my_it >= 0) {
-      const int b = (int)(my_it / a.Hkv);
+      const int b = my_it / a.Hkv;
       const int c = (int)(x - my_s);
-      const int64_t key = (int64_t)c * 16;
-      const int64_t e = key / a.page_size;
-      m_row = (int)(key - e * a.page_size);
+      m_g = my_it - b * a.Hkv;
+      const int e = c / (a.page_size >> 4);
+      m_row = 16 * (c - e * (a.page_size >> 4));
       m_c = c;
-      int64_t lp = e;
-      if (a.page_list != nullptr) lp = a.page_list[my_it * a.list_stride + e];
+      int lp = e;
+      if (a.page_list != nullptr) lp = a.page_list[(int64_t)my_it * a.list_stride + e];
       if (lp >= 0 && lp < a.max_pages) {
-        const int64_t j0 = lp * a.page_size + m_row;
+        const int64_t j0 = (int64_t)lp * a.page_size + m_row;
         if (j0 < a.seq_lens[b]) {
           const int phys = a.block_table[(int64_t)b * a.max_pages + lp];
           if (phys >= 0 && phys < a.num_pages) {
@@ -252,58 +322,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const uint32_t bar0 = smem_addr(smem + C::kBarOff) + 8 * (warp * S);
   const uint32_t ring = sbase + warp * (S * C::kSlot);
-  int sl_item[S], sl_j0[S], sl_c[S];
-#pragma unroll
-  for (int s = 0; s < S; ++s) sl_item[s] = sl_j0[s] = -1, sl_c[s] = 0;
-  auto issue = [&](int k, int s) {  // unit k into slot s
-    if ((k & 31) == 0) load_batch(k);
-    const int item = __shfl_sync(0xffffffffu, m_item, k & 31);
-    const int phys = __shfl_sync(0xffffffffu, m_phys, k & 31);
-    const int row = __shfl_sync(0xffffffffu, m_row, k & 31);
-    sl_item[s] = item;
-    sl_j0[s] = __shfl_sync(0xffffffffu, m_j0, k & 31);
-    sl_c[s] = __shfl_sync(0xffffffffu, m_c, k & 31);
-    if (lane == 0) {
-      if (phys >= 0) {
-        const int g = item % a.Hkv;
-        mbar_arrive_expect_tx(bar0 + 8 * s, (uint32_t)C::kSlot);
-        const uint32_t st = ring + s * C::kSlot;
-#pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) {
-          tma_load_4d(st + c * 2048, &tm_k, bar0 + 8 * s, c * 64, g, row, phys);
-          tma_load_4d(st + C::kHalf + c * 2048, &tm_v, bar0 + 8 * s, c * 64, g, row, phys);
-        }
+  int4* meta = reinterpret_cast<int4*>(smem + C::kMetaOff) + warp * C::kMeta;
+  auto issue = [&](int h, int slot) {  // keys (even) or values (odd) of unit h / 2
+    const int k = h >> 1;
+    if ((h & 63) == 0) load_batch(k);
+    if (lane == (k & 31)) {
+      const uint32_t bar = bar0 + 8 * slot;
+      if ((h & 1) == 0) meta[k % C::kMeta] = make_int4(m_item, m_j0, m_c, 0);
+      if (m_phys >= 0) {
+        mbar_arrive_expect_tx(bar, (uint32_t)C::kSlot);
+        tma_load_5d(ring + slot * C::kSlot, (h & 1) ? &tm_v : &tm_k, bar, m_row, m_g, m_phys);
       } else {
-        mbar_arrive(bar0 + 8 * s);  // nothing to fetch; the phase completes all the same
+        mbar_arrive(bar);  // nothing to fetch; the phase completes all the same
       }
     }
   };
-#pragma unroll
-  for (int s = 0; s < S; ++s)
-    if (s < cnt) issue(s, s);
-  __syncthreads();  // key factors are ready
 
   // ---- per-item state
-  const int c4 = lane & 3;       // column group of the mma fragments
-  const int hrow = lane >> 2;    // M row of this lane
-  const int hq = kPack ? (hrow & 3) : hrow;  // query head of that row
-  uint32_t qf[KS][2];            // base query fragments: dims 16 ks + 2 c4 (+ 8) of head hq
+  uint32_t qf[KS][2];                 // base query fragments: dims 16 ks + 2 c4 (+ 8) of head hq
   float oacc[D / 16][4];
   float m_used = -INFINITY, l_part = 0.f;
   int item = -1, seg_c = 0, seg_k = 0;  // current item, its unit index at the segment's first unit k
   int L = 0, local_from = 0, G = 1;
   bool all_local = true;
-  int64_t dq = 0;
-  uint32_t g_magic = 0;
+  int dq = 0;
+  uint32_t g_inv = 0;
   const float sl2 = a.scale_log2;
 #pragma unroll
   for (int n = 0; n < D / 16; ++n) oacc[n][0] = oacc[n][1] = oacc[n][2] = oacc[n][3] = 0.f;
 
-  // Writes the warp's accumulated segment as a partial (m, l, o): heads at rows of `p`.
-  auto store_partial = [&](const Partial& p) {
+  // The segment's sum of this lane's head.
+  auto head_sum = [&]() {
     float l = l_part;
     l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    return l + __shfl_xor_sync(0xffffffffu, l, 2);
+  };
+  // The output of head 2 c4 + (k & 1), dim 16 mt + hrow + (k & 2 ? 8 : 0).
+  auto out_value = [&](int mt, int k) {
+    float v = oacc[mt][k];
+    if (kPack) v += __shfl_down_sync(0xffffffffu, v, 2);  // + the lo parts' product, four columns on
+    return v;
+  };
+  // Writes the warp's accumulated segment as a partial (m, l, o).
+  auto store_partial = [&](const Partial& p) {
+    const float l = head_sum();
     if (c4 == 0 && hrow < r) {
       p.m[hrow] = m_used;
       p.l[hrow] = l;
@@ -312,18 +374,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float v = oacc[mt][k];
-        if (kPack) v += __shfl_down_sync(0xffffffffu, v, 2);  // + the lo parts' product, four columns on
+        const float v = out_value(mt, k);
         const int h = 2 * c4 + (k & 1);
-        const int d = 16 * mt + hrow + ((k & 2) ? 8 : 0);
-        if (h < r) p.o[h * D + d] = v;
+        if (h < r) p.o[h * D + 16 * mt + hrow + ((k & 2) ? 8 : 0)] = v;
       }
   };
   // The whole item was this warp's: normalise and write the results.
   auto store_final = [&](int it) {
-    float l = l_part;
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const float l = head_sum();
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
     const int b = it / a.Hkv, g = it - b * a.Hkv;
     const int64_t row = (int64_t)b * a.Hq + g * r;
@@ -334,33 +392,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float v = oacc[mt][k];
-        if (kPack) v += __shfl_down_sync(0xffffffffu, v, 2);
+        const float v = out_value(mt, k) * ((k & 1) ? i1 : i0);
         const int h = 2 * c4 + (k & 1);
-        const int d = 16 * mt + hrow + ((k & 2) ? 8 : 0);
-        if (h < r) a.o[(row + h) * D + d] = __float2bfloat16_rn(v * ((k & 1) ? i1 : i0));
+        if (h < r) a.o[(row + h) * D + 16 * mt + hrow + ((k & 2) ? 8 : 0)] = __float2bfloat16_rn(v);
       }
   };
+  constexpr int kQLanes = kPack ? 16 : 32;     // lanes with fragments of their own
+  const int qlane = hq * 4 + c4;
+  uint4* qbuf = reinterpret_cast<uint4*>(smem + C::kQOff + warp * C::kQBytes);  // [k-step][x, y][lane]
+  const uint32_t qaddr = smem_addr(qbuf) + qlane * 16;
+  int jb = -1, qb = 0;  // the queries in qbuf are turned for position jb; floor(jb / G)
+  const float4* csb = reinterpret_cast<const float4*>(smem + C::kCsOff + warp * D * 4);
+  // row kr of a 16-row tile, 16-byte pieces 2 m + (bit) exclusive-or the row's low bits:
+  // keys take rows (lane >> 4) * 8 + (lane & 7) and bit (lane >> 3) & 1, and so do the values
+  const int kr = (lane >> 4) * 8 + (lane & 7);
+  const uint32_t tile_off = kr * 128 + ((((lane >> 3) & 1) ^ (kr & 7)) << 4);
 
   bool ok = true;
-  int k_fail = 0;
-  int tail_item = -1, head_item = -1;
-  for (int k0 = 0; k0 < cnt && ok; k0 += S) {
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int k = k0 + s;
-      if (k >= cnt || !ok) break;
-      if (sl_item[s] != item) {
-        if (item >= 0) {  // the previous item ends here, inside the warp's range
-          if (wb + seg_k - seg_c >= wb) {
+  int h_next = 0;
+  int slot = 0;         // of the half unit at hand; the half S further on takes it over
+  uint32_t phase = 0;   // how often the ring went round, mod 2
+  auto wait = [&]() {
+    ok = mbar_wait(bar0 + 8 * slot, phase, abort_flag, a.dev_error);
+    ok = __all_sync(0xffffffffu, ok);
+    return ok;
+  };
+  auto pass_on = [&](int h) {  // half unit h is read: refill its slot, step to the next
+    __syncwarp();
+    if (h + S < 2 * cnt) issue(h + S, slot);
+    if (++slot == S) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  };
+  for (int h = 0; h < S && h < 2 * cnt; ++h) issue(h, h);
+  __syncwarp();
+  // The step behind the last unit closes the last segment.
+#pragma unroll 1
+  for (int k = -1; k <= cnt; ++k) {
+    if (k == -1) {
+      // The first units are on their way; meanwhile the CTA forms its tables.
+      constexpr int kRowsAtOnce = D == 128 ? 1 : 2;  // rows of R(-e) that a warp's lanes cover
+      for (int e = kRowsAtOnce * warp + (D == 128 ? 0 : lane >> 4); e < C::kERows; e += kRowsAtOnce * kWarps) {
+        float4 f;
+        sincos_phase(-e, turn0, &f.z, &f.x);
+        sincos_phase(-e, turn1, &f.w, &f.y);
+        *reinterpret_cast<float4*>(smem + C::kEOff + e * C::kERow + qt * 8) = f;
+      }
+      __syncthreads();
+    }
+    if (k >= 0) {
+      int4 md = make_int4(-1, -1, 0, 0);
+      if (k < cnt) md = meta[k % C::kMeta];
+      if (cnt == 0) break;
+      if (md.x != item) {
+        if (item >= 0) {  // the segment in hand ends here
+          const bool began = seg_k >= seg_c;
+          const int64_t first = wb + seg_k - seg_c;
+          const int n = k == cnt || !began ? item_units(a, item) : 0;
+          const bool ends = k < cnt || first + n <= we;
+          if (began && ends) {
             store_final(item);
-          } else {
+          } else if (k < cnt) {  // begun before this warp's range
             store_partial(partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + warp, r, D));
-            head_item = item;
+            if (lane == 0) ent[2 * warp] = {first, n, item};
+          } else {  // ends with the range or runs on; the warp's ring is free for it
+            store_partial(partial_at(reinterpret_cast<float*>(smem), warp, r, D, S * C::kSlot / 4));
+            if (lane == 0) ent[2 * warp + 1] = {first, n, item};
           }
         }
-        item = sl_item[s];
-        seg_c = sl_c[s];
+        if (k == cnt) break;
+        item = md.x;
+        seg_c = md.z;
         seg_k = k;
         m_used = -INFINITY;
         l_part = 0.f;
@@ -370,8 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         L = a.seq_lens[b];
         G = (int)group_size(L, a.w_pretrained);
         all_local = jl::all_local(L, a.w0, G);
-        dq = query_remote(L - 1, G, query_shift(a.w0, G, a.qshift)) - (L - 1);
-        g_magic = G < 16 ? (uint32_t)((((uint64_t)1 << 32) + (uint64_t)G - 1) / (uint64_t)G) : 0u;
+        dq = (int)(query_remote(L - 1, G, query_shift(a.w0, G, a.qshift)) - (L - 1));
+        g_inv = (uint32_t)(((uint64_t)1 << 32) / (uint64_t)(G > 1 ? G : 2));
+        jb = -1;
         local_from = all_local ? 0 : L - a.w0;  // keys j >= local_from are scored with base RoPE
         const __nv_bfloat16* qp = a.q + ((int64_t)b * a.Hq + g * r + hq) * D + 2 * c4;
 #pragma unroll
@@ -380,93 +484,93 @@ __global__ void __launch_bounds__(kThreads, 1)
           qf[ks][1] = hq < r ? *reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8) : 0u;
         }
       }
-      const int j0 = sl_j0[s];
-      const bool t_local = all_local || j0 >= local_from;
-      const bool t_remote = !all_local && (j0 + 15 < local_from);
-      float* csb = reinterpret_cast<float*>(smem + C::kCsOff) + warp * D;
-      int rm = 0;
-      if (j0 >= 0 && !t_local) {
-        const int qd = j0 / G;
-        rm = j0 - qd * G;
-        const int64_t turn = dq - ((int64_t)qd - j0);
-#pragma unroll
-        for (int e = 0; e < H2 / 32; ++e) {
-          const int t = lane + 32 * e;
-          float sn, cs;
-          sincos_turns(turn, utab[t].x, utab[t].y, &sn, &cs);
-          csb[(t >> 1) * 4 + (t & 1)] = cs;
-          csb[(t >> 1) * 4 + 2 + (t & 1)] = sn;
+      const int j0 = md.y;
+      const bool any_local = all_local || j0 + 15 >= local_from;
+      const bool any_remote = !all_local && j0 < local_from;
+      uint32_t ef[2] = {0u, 0u};  // factor rows of this lane's keys hrow and 8 + hrow
+      if (j0 >= 0 && any_remote) {
+        // floor(j0 / G) by the reciprocal rounded down (at most one short)
+        int qd = (int)__umulhi((unsigned)j0, g_inv), rm = j0 - qd * G;
+        if (rm >= G) {
+          rm -= G;
+          ++qd;
         }
-        __syncwarp();
+        // Turned queries serve while the keys' own turns from where they were formed,
+        // e = (j0 + u - jb) - (floor((j0 + u) / G) - floor(jb / G)), stay in the table.
+        int off = (j0 - jb) - (qd - qb);
+        if (jb < 0 || j0 < jb || off > C::kERows - 16) {
+          jb = j0;
+          qb = qd;
+          off = 0;
+          float4 f;
+          sincos_phase(dq - (qd - j0), turn0, &f.z, &f.x);
+          sincos_phase(dq - (qd - j0), turn1, &f.w, &f.y);
+          __syncwarp();
+          *reinterpret_cast<float4*>(smem + C::kCsOff + warp * D * 4 + qt * 8) = f;  // (D = 64: twice the same)
+          __syncwarp();
+          // packed heads sit in two lanes each: either turns every other k-step
+#pragma unroll
+          for (int i = 0; i < (kPack ? KS2 / 2 : KS2); ++i) {
+            const int kp = kPack ? 2 * i + (hrow >> 2) : i;
+            uint32_t q0, q1, q2, q3;
+            if (kPack) {  // qf[kp], qf[kp + KS2] without indexing registers
+              q0 = hrow < 4 ? qf[2 * i][0] : qf[2 * i + 1][0];
+              q1 = hrow < 4 ? qf[2 * i][1] : qf[2 * i + 1][1];
+              q2 = hrow < 4 ? qf[2 * i + KS2][0] : qf[2 * i + 1 + KS2][0];
+              q3 = hrow < 4 ? qf[2 * i + KS2][1] : qf[2 * i + 1 + KS2][1];
+            } else {
+              q0 = qf[i][0], q1 = qf[i][1], q2 = qf[i + KS2][0], q3 = qf[i + KS2][1];
+            }
+            uint4 lo, hi;
+            rot_split_bf16(q0, q2, csb[8 * kp + c4], lo.x, lo.y, hi.x, hi.y);
+            rot_split_bf16(q1, q3, csb[8 * kp + 4 + c4], lo.z, lo.w, hi.z, hi.w);
+            qbuf[(kp * 2) * kQLanes + qlane] = lo;
+            qbuf[(kp * 2 + 1) * kQLanes + qlane] = hi;
+          }
+          __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int u = 8 * i + hrow;
+          const int x = rm + u;  // below G + 16
+          int qe = (int)__umulhi((unsigned)x, g_inv);
+          if (x - qe * G >= G) ++qe;
+          ef[i] = sbase + C::kEOff + (off + u - qe) * C::kERow + c4 * 16;
+        }
       }
-
-      ok = mbar_wait(bar0 + 8 * s, (uint32_t)(k0 / S) & 1u, abort_flag, a.dev_error);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {
-        k_fail = k;
-        break;
-      }
-
+      h_next = 2 * k;
+      if (!wait()) break;
+      const uint32_t kst = ring + slot * C::kSlot + tile_off;
+      float x[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
       if (j0 >= 0) {
-        const uint32_t kst = ring + s * C::kSlot;
-        const uint32_t vst = kst + C::kHalf;
-        float sloc[2][4], sah[2][4], sal[2][4];
+        // This lane's scores: keys 8 nt + 2 c4 + {0, 1} of head hq.  A unit on the
+        // band's edge forms both kinds and each key keeps its own.
+        if (any_remote) {
+          // hi and lo parts of the keys in accumulators of their own, of the queries in
+          // rows h and h + 8: the sum of all four is (q_hi + q_lo) . (k_hi + k_lo)
+          float sah[2][4], sal[2][4];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+          for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sloc[nt][e] = sah[nt][e] = sal[nt][e] = 0.f;
-
-        // factor rows of this lane's two keys (one per 8-key n-tile):
-        // e(u) = u - (floor((j0 + u) / G) - floor(j0 / G))
-        const float4* Er[2];
+            for (int e = 0; e < 4; ++e) sah[nt][e] = sal[nt][e] = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int u = 8 * nt + (lane >> 2);
-          const int q = G >= 16 ? (rm + u >= G ? 1 : 0) : (int)__umulhi((unsigned)(rm + u), g_magic);
-          Er[nt] = reinterpret_cast<const float4*>(smem + C::kEOff + (u - (G == 1 ? u : q)) * C::kERow);
-        }
-        const float4* Qf = reinterpret_cast<const float4*>(csb);
-
-#pragma unroll
-        for (int kp = 0; kp < KS2; ++kp) {
-          uint32_t klo[4], khi[4];
-          {
-            const int mi = lane >> 3;
-            const int kr = (mi >> 1) * 8 + (lane & 7);
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const int ks = kp + hf * KS2;
-              const int u = 2 * (ks & 3) + (mi & 1);
-              const uint32_t addr = kst + (ks >> 2) * 2048 + kr * 128 + ((u ^ (kr & 7)) << 4);
-              if (hf == 0)
-                ldsm_x4(addr, klo[0], klo[1], klo[2], klo[3]);
-              else
-                ldsm_x4(addr, khi[0], khi[1], khi[2], khi[3]);
-            }
-          }
-          if (!t_remote) {  // local or straddling: base query, keys as stored
-            const uint32_t alo[4] = {qf[kp][0], 0u, qf[kp][1], 0u};
-            const uint32_t ahi[4] = {qf[kp + KS2][0], 0u, qf[kp + KS2][1], 0u};
+          for (int kp = 0; kp < KS2; ++kp) {
+            // k-step kp holds the first coordinate of pairs t in [16 kp, 16 kp + 16), k-step
+            // kp + D/32 the second, so each pair is complete in registers
+            uint32_t klo[4], khi[4], kah[4], kal[4], kbh[4], kbl[4], alo[4], ahi[4];
+            load_keys<D>(kst, kp, klo);
+            load_keys<D>(kst, kp + KS2, khi);
+            lds_u4(qaddr + (kp * 2) * kQLanes * 16, alo);
+            lds_u4(qaddr + (kp * 2 + 1) * kQLanes * 16, ahi);
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-              mma_bf16(sloc[nt], alo, klo[2 * nt], klo[2 * nt + 1]);
-              mma_bf16(sloc[nt], ahi, khi[2 * nt], khi[2 * nt + 1]);
-            }
-          }
-          if (!t_local) {  // remote or straddling: corrected query and keys
-            uint32_t kah[4], kal[4], kbh[4], kbl[4];
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              const float4 f01 = Er[nt][(16 * kp + 2 * c4) >> 1];
-              const float4 f23 = Er[nt][(16 * kp + 8 + 2 * c4) >> 1];
+              float4 f01, f23;
+              lds_f4(ef[nt] + kp * 128, f01);
+              lds_f4(ef[nt] + kp * 128 + 64, f23);
               rot_split_bf16(klo[2 * nt], khi[2 * nt], f01, kah[2 * nt], kal[2 * nt], kbh[2 * nt], kbl[2 * nt]);
               rot_split_bf16(klo[2 * nt + 1], khi[2 * nt + 1], f23, kah[2 * nt + 1], kal[2 * nt + 1],
                              kbh[2 * nt + 1], kbl[2 * nt + 1]);
             }
-            uint32_t alo[4], ahi[4];
-            rot_split_bf16(qf[kp][0], qf[kp + KS2][0], Qf[(16 * kp + 2 * c4) >> 1], alo[0], alo[1], ahi[0], ahi[1]);
-            rot_split_bf16(qf[kp][1], qf[kp + KS2][1], Qf[(16 * kp + 8 + 2 * c4) >> 1], alo[2], alo[3], ahi[2],
-                           ahi[3]);
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
               mma_bf16(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
@@ -475,34 +579,56 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_bf16(sal[nt], ahi, kbl[2 * nt], kbl[2 * nt + 1]);
             }
           }
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              x[nt][e] = (sah[nt][e] + sah[nt][e + 2]) + (sal[nt][e] + sal[nt][e + 2]);
         }
-
-        // scores in log2 units, the band's choice and the mask behind the sequence
-        float x[2][2];
+        if (any_local) {  // base query, keys as stored
+          float sb[2][4];
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sb[nt][e] = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            uint32_t kk[4];
+            load_keys<D>(kst, ks, kk);
+            const uint32_t aq[4] = {qf[ks][0], 0u, qf[ks][1], 0u};
+            mma_bf16(sb[0], aq, kk[0], kk[1]);
+            mma_bf16(sb[1], aq, kk[2], kk[3]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!any_remote || j0 + 8 * nt + 2 * c4 + e >= local_from) x[nt][e] = sb[nt][e];
+        }
+      }
+      pass_on(2 * k);
+      h_next = 2 * k + 1;
+      if (!wait()) break;
+      if (j0 >= 0) {
+        const uint32_t vst = ring + slot * C::kSlot + tile_off;
+        // log2 units, the mask behind the sequence, and the running maximum of the lane's head
+        const bool tail = j0 + 16 > L;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int j = j0 + 8 * nt + 2 * c4 + e;
-            const bool loc = all_local || j >= local_from;
-            const float rem = (sah[nt][e] + sah[nt][e + 2]) + (sal[nt][e] + sal[nt][e + 2]);
-            float v = (loc ? sloc[nt][e] : rem) * sl2;
-            if (j >= L) v = -INFINITY;
-            x[nt][e] = v;
+            x[nt][e] *= sl2;
+            if (tail && j0 + 8 * nt + 2 * c4 + e >= L) x[nt][e] = -INFINITY;
           }
         float mt = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
         mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-        float alpha = 1.f;
-        bool resc = false;
-        if (mt > m_used + 8.f) {  // a running maximum up to 2^8 behind keeps every p below 2^8
-          alpha = (m_used == -INFINITY) ? 0.f : ex2_approx(m_used - mt);
-          resc = m_used != -INFINITY;
+        const bool grow = mt > m_used + 8.f;  // a maximum up to 2^8 behind keeps every p below 2^8
+        if (__any_sync(0xffffffffu, grow)) {
+          const float alpha = grow ? ex2_approx(m_used - mt) : 1.f;  // 0 for the first keys
           l_part *= alpha;
-          m_used = mt;
-        }
-        if (__any_sync(0xffffffffu, resc)) {
-          // this lane's O^T columns are heads 2 c4 and 2 c4 + 1
+          if (grow) m_used = mt;
+          // this lane's O^T columns are heads 2 c4 and 2 c4 + 1 (and, packed, their lo parts)
           const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c4);
           const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * c4 + 4);
 #pragma unroll
@@ -514,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float msub = (m_used == -INFINITY) ? 0.f : m_used;
-        uint32_t ph[2], pl[2];
+        uint32_t ph[2], pl[2];  // P^T fragments are the lane's own scores
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           const float p0 = ex2_approx(x[nt][0] - msub), p1 = ex2_approx(x[nt][1] - msub);
@@ -523,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t pb0 = kPack && hrow >= 4 ? pl[0] : ph[0];
         const uint32_t pb1 = kPack && hrow >= 4 ? pl[1] : ph[1];
-        const bool tail = j0 + 16 > L;  // rows behind the sequence hold anything, NaN included
+        // rows behind the sequence hold anything, NaN included
         uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
         if (tail) {
           const int u = L - j0 - 2 * c4;  // of the keys 2 c4 + {0, 1} and 8 + 2 c4 + {0, 1}
@@ -532,10 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int mt2 = 0; mt2 < D / 16; ++mt2) {
-          const int mi = lane >> 3;
-          const int kr = (mi >> 1) * 8 + (lane & 7);
-          const int u = 2 * (mt2 & 3) + (mi & 1);
-          const uint32_t addr = vst + (mt2 >> 2) * 2048 + kr * 128 + ((u ^ (kr & 7)) << 4);
+          const uint32_t addr = (vst ^ ((mt2 & 3) << 5)) + (mt2 >> 2) * 2048;
           uint32_t va[4];
           ldsm_x4_t(addr, va[0], va[1], va[2], va[3]);
           if (tail) {
@@ -548,150 +671,150 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!kPack) mma_bf16(oacc[mt2], va, pl[0], pl[1]);
         }
       }
-      __syncwarp();  // every lane has read the slot (and the query factors)
-      if (k + S < cnt) issue(k + S, s);
+      pass_on(2 * k + 1);
+      __syncwarp();  // a description may have been written
     }
   }
   if (!ok) {
-    // Gave up at unit k_fail: let the copies in flight land (again with a limit)
-    // before the ring is reused or the CTA ends.
+    // Gave up at half unit h_next: let the copies in flight land (again with a limit)
+    // before the CTA goes on.
     const uint64_t t0 = global_timer_ns();
-    for (int k = k_fail; k < min(cnt, k_fail + S); ++k)
-      while (!mbar_try_wait(bar0 + 8 * (k % S), (uint32_t)(k / S) & 1u))
+    for (int h = h_next; h < min(2 * cnt, h_next + S); ++h)
+      while (!mbar_try_wait(bar0 + 8 * (h % S), (uint32_t)(h / S) & 1u))
         if (global_timer_ns() - t0 > 100000000ull) break;
-  }
-
-  // ---- the segment in hand: an item that ended with the range, or runs on
-  Partial tails;
-  __syncthreads();  // every warp is done with its ring; it holds the partials from here
-  {
-    tails = partial_at(reinterpret_cast<float*>(smem), warp, r, D);
-    if (item >= 0) {
-      const bool began = wb + seg_k - seg_c >= wb;
-      const bool ends = wb + seg_k - seg_c + item_units(a, item) <= we;
-      if (began && ends) {
-        store_final(item);
-      } else {
-        store_partial(tails);
-        tail_item = item;
-      }
-    }
-    if (lane == 0) {
-      ent_item[2 * warp] = head_item;
-      ent_item[2 * warp + 1] = tail_item;
-    }
   }
   __syncthreads();
 
-  // ---- join the warps' partials item by item; entries 2 w (head) and 2 w + 1 (tail) are in unit order
-  auto entry = [&](int e) -> Partial {
-    return (e & 1) ? partial_at(reinterpret_cast<float*>(smem), e >> 1, r, D)
-                   : partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + (e >> 1), r, D);
+  // ---- join the warps' partials, item by item in unit order.  An item's parts are the
+  // tails of neighbouring warps and at most one head, of the warp behind them.
+  auto row_of = [&](int it) -> int64_t { return (int64_t)(it / a.Hkv) * a.Hq + (it % a.Hkv) * r; };
+  auto write_result = [&](int64_t row, int idx, float o, float M, float l) {
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    a.o[row * D + idx] = __float2bfloat16_rn(o * inv);
+    if (idx % D == 0 && a.lse != nullptr)
+      a.lse[row + idx / D] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.69314718055994531f;
   };
+  // A part's weight 2^(m - M): an empty part's sum is 0, and a NaN that left the maximum at -inf goes through.
+  auto weight = [](float m, float l, float M) { return m == -INFINITY ? l : ex2_approx(m - M); };
   int shared_item[2] = {-1, -1};  // items shared with the CTAs before and behind
-  for (int e0 = 0; e0 < 2 * kWarps;) {
-    const int it = ent_item[e0];
-    if (it < 0) {
-      ++e0;
-      continue;
-    }
-    int e1 = e0 + 1;
-    while (e1 < 2 * kWarps && (ent_item[e1] < 0 || ent_item[e1] == it)) ++e1;
-    // the item's place on the line
-    int64_t s = 0;
-    {
-      const int64_t seg = it / per_thread;
-      s = scan[seg];
-      for (int64_t i = seg * per_thread; i < it; ++i) s += item_units(a, i);
-    }
-    const int64_t n = item_units(a, it);
-    const bool whole = s >= c0 && s + n <= c1;
+  int shared_n[2] = {0, 0};
+  int64_t shared_s[2] = {0, 0};
+  int done = -1;
+#pragma unroll 1
+  for (int e = 0; e < 2 * kWarps; ++e) {  // heads at 2 w, tails at 2 w + 1
+    const int it = ent[e].item;
+    if (it < 0 || it == done) continue;
+    done = it;
+    int head = -1;  // the warp whose head this item is
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      if (ent[2 * w].item == it) head = w;
+    const int64_t s = ent[e].s;
+    const bool whole = s >= c0 && s + ent[e].n <= c1;
     const int slot = s < c0 ? 0 : 1;
-    if (!whole) shared_item[slot] = it;
+    if (!whole) {
+      shared_item[slot] = it;
+      shared_s[slot] = s;
+      shared_n[slot] = ent[e].n;
+    }
     const Partial out = partial_at(a.cta_parts, (int64_t)blockIdx.x * 2 + slot, r, D);
-    const int b = it / a.Hkv, g = it - b * a.Hkv;
-    const int64_t row = (int64_t)b * a.Hq + g * r;
+    const Partial hp = partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + (head < 0 ? 0 : head), r, D);
     for (int idx = tid; idx < r * D; idx += kThreads) {
       const int h = idx / D;
-      float M = -INFINITY;
-      for (int e = e0; e < e1; ++e)
-        if (ent_item[e] >= 0) M = fmaxf(M, entry(e).m[h]);
-      float o = 0.f, l = 0.f;
-      for (int e = e0; e < e1; ++e) {
-        if (ent_item[e] < 0) continue;
-        const Partial p = entry(e);
-        // an empty part's sum is 0; a NaN that left the maximum at -inf goes through
-        const float wt = p.m[h] == -INFINITY ? p.l[h] : ex2_approx(p.m[h] - M);
-        o += wt * p.o[idx];
-        l += wt * p.l[h];
+      float m[kWarps + 1], l[kWarps + 1], M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const Partial p = partial_at(reinterpret_cast<float*>(smem), w, r, D, S * C::kSlot / 4);
+        const bool in = ent[2 * w + 1].item == it;
+        m[w] = in ? p.m[h] : -INFINITY;
+        l[w] = in ? p.l[h] : 0.f;
+        M = fmaxf(M, m[w]);
+      }
+      m[kWarps] = head < 0 ? -INFINITY : hp.m[h];
+      l[kWarps] = head < 0 ? 0.f : hp.l[h];
+      M = fmaxf(M, m[kWarps]);
+      float o = 0.f, lsum = 0.f;
+#pragma unroll
+      for (int w = 0; w <= kWarps; ++w) {
+        const Partial p = partial_at(reinterpret_cast<float*>(smem), w < kWarps ? w : 0, r, D, S * C::kSlot / 4);
+        const bool in = w < kWarps ? ent[2 * w + 1].item == it : head >= 0;
+        const float wt = weight(m[w], l[w], M);
+        const float v = w < kWarps ? p.o[idx] : (head < 0 ? 0.f : hp.o[idx]);
+        if (in) o += wt * v;  // (a ring that holds no part holds anything)
+        lsum += wt * l[w];
       }
       if (whole) {
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        a.o[row * D + idx] = __float2bfloat16_rn(o * inv);
-        if (idx == h * D && a.lse != nullptr)
-          a.lse[row + h] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.69314718055994531f;
+        write_result(row_of(it), idx, o, M, lsum);
       } else {
         out.o[idx] = o;
-        if (idx == h * D) {
+        if (idx % D == 0) {
           out.m[h] = M;
-          out.l[h] = l;
+          out.l[h] = lsum;
         }
       }
     }
-    e0 = e1;
   }
 
   // ---- join the CTAs' partials: the item's last ticket does it
-  auto cta_of = [&](int64_t unit) -> int64_t { return ((unit + 1) * N - 1) / U; };
+  float* wts = reinterpret_cast<float*>(smem + C::kWtsOff);  // [r][kMaxParts]
+  float* tot = wts + kMaxR * C::kMaxParts;                   // [r] maxima, then [r] sums
+  auto cta_of = [&](int64_t unit) -> int { return (int)(((unit + 1) * N - 1) / U); };
 #pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
     const int it = shared_item[slot];
     if (it < 0) continue;  // the same for every thread of the CTA
-    int64_t s = 0;
-    {
-      const int64_t seg = it / per_thread;
-      s = scan[seg];
-      for (int64_t i = seg * per_thread; i < it; ++i) s += item_units(a, i);
-    }
-    const int64_t first = cta_of(s), last = cta_of(s + item_units(a, it) - 1);
+    const int first = cta_of(shared_s[slot]), last = cta_of(shared_s[slot] + shared_n[slot] - 1);
     __threadfence();
     __syncthreads();
     if (tid == 0) *ticket = atomicInc(&a.counters[first], (unsigned)(last - first)) == (unsigned)(last - first);
     __syncthreads();
     if (*ticket == 0) continue;
     __threadfence();
-    const int b = it / a.Hkv, g = it - b * a.Hkv;
-    const int64_t row = (int64_t)b * a.Hq + g * r;
-    for (int idx = tid; idx < r * D; idx += kThreads) {
-      const int h = idx / D;
-      // the item begins inside the first CTA's range (slot 1) and before the others' (slot 0)
-      auto part = [&](int64_t c) { return partial_at(a.cta_parts, c * 2 + (c == first ? 1 : 0), r, D); };
+    const int n = last - first + 1;
+    // the item begins inside the first CTA's range (slot 1) and before the others' (slot 0)
+    const int64_t step = 2 * decode_partial_floats(r, D);
+    const float* parts = a.cta_parts + first * step;
+    for (int h = warp; h < r; h += kWarps) {  // weights, one warp per head
+      auto ml = [&](int c) { return parts + c * step + (c == 0 ? step / 2 : 0) + h; };
       float M = -INFINITY;
-      for (int64_t c = first; c <= last; ++c) M = fmaxf(M, __ldcg(part(c).m + h));
-      float o = 0.f, l = 0.f;
-      for (int64_t c = first; c <= last; ++c) {
-        const Partial p = part(c);
-        const float mc = __ldcg(p.m + h);
-        const float lc = __ldcg(p.l + h);
-        const float wt = mc == -INFINITY ? lc : ex2_approx(mc - M);
-        o += wt * __ldcg(p.o + idx);
+      for (int c = lane; c < n; c += 32) M = fmaxf(M, __ldcg(ml(c)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      float l = 0.f;
+      for (int c = lane; c < n; c += 32) {
+        const float mc = __ldcg(ml(c)), lc = __ldcg(ml(c) + r);
+        const float wt = weight(mc, lc, M);
+        wts[h * C::kMaxParts + c] = wt;
         l += wt * lc;
       }
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-      a.o[row * D + idx] = __float2bfloat16_rn(o * inv);
-      if (idx == h * D && a.lse != nullptr)
-        a.lse[row + h] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.69314718055994531f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) {
+        tot[h] = M;
+        tot[kMaxR + h] = l;
+      }
     }
+    __syncthreads();
+    for (int idx = tid; idx < r * D; idx += kThreads) {
+      const int h = idx / D;
+      const float* w = wts + h * C::kMaxParts;
+      const float* po = parts + 2 * r + idx;
+      float o = w[0] * __ldcg(po + step / 2);
+#pragma unroll 8
+      for (int c = 1; c < n; ++c) o += w[c] * __ldcg(po + c * step);
+      write_result(row_of(it), idx, o, tot[h], tot[kMaxR + h]);
+    }
+    __syncthreads();  // wts and tot may be written again
   }
 }
 
 template <int D, bool kPack>
-cudaError_t launch_dp(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedDecodeArgs& a, int ctas,
+cudaError_t launch_dp(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedDecodeArgs& a,
                       cudaStream_t stream) {
   auto k = paged_decode_kernel<D, kPack>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PgCfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  k<<<ctas, kThreads, PgCfg<D>::kSmem, stream>>>(tm_k, tm_v, a);
+  k<<<decode_paged_max_ctas(), kThreads, PgCfg<D>::kSmem, stream>>>(tm_k, tm_v, a);  // one CTA per SM
   return cudaGetLastError();
 }
 
@@ -702,18 +825,15 @@ int decode_paged_max_ctas() {
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
     return 148;
-  return n;
+  return n < PgCfg<128>::kMaxParts ? n : PgCfg<128>::kMaxParts;
 }
 int decode_paged_warps() { return kWarps; }
 
 cudaError_t launch_decode_paged(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedDecodeArgs& a, int D,
                                 cudaStream_t stream) {
-  const int ctas = decode_paged_max_ctas();  // one per SM
   if (D == 128)
-    return a.r <= 4 ? launch_dp<128, true>(tm_k, tm_v, a, ctas, stream)
-                    : launch_dp<128, false>(tm_k, tm_v, a, ctas, stream);
-  return a.r <= 4 ? launch_dp<64, true>(tm_k, tm_v, a, ctas, stream)
-                  : launch_dp<64, false>(tm_k, tm_v, a, ctas, stream);
+    return a.r <= 4 ? launch_dp<128, true>(tm_k, tm_v, a, stream) : launch_dp<128, false>(tm_k, tm_v, a, stream);
+  return a.r <= 4 ? launch_dp<64, true>(tm_k, tm_v, a, stream) : launch_dp<64, false>(tm_k, tm_v, a, stream);
 }
 
 }  // namespace jl

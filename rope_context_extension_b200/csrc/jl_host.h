@@ -54,9 +54,11 @@ inline void fill_turns(double* u_hi, double* u_lo, const double* theta, int D) {
 
 inline float resolve_scale(float s, int D) { return s == 0.f ? 1.0f / std::sqrt((float)D) : s; }
 
-// theta_t / (2 pi) of one (head_dim, rope_base), as fill_turns splits it.
+// theta_t / (2 pi) of one (head_dim, rope_base), as fill_turns splits it and its
+// fraction in 64-bit fixed point.
 struct TurnTable {
   double hi[kMaxHalfDim], lo[kMaxHalfDim];
+  uint64_t fixed[kMaxHalfDim];
 };
 
 // The table for (D, base).  Each thread keeps the last one it formed (64 pow and
@@ -72,6 +74,10 @@ inline const TurnTable& turn_table(int D, double base) {
     double theta[kMaxHalfDim];
     fill_theta(theta, D, base);
     fill_turns(last.t.hi, last.t.lo, theta, D);
+    for (int t = 0; t < D / 2; ++t) {
+      const double u = theta[t] / 6.283185307179586;  // whole turns of theta itself change no integer multiple
+      last.t.fixed[t] = (uint64_t)std::ldexp(u - std::floor(u), 64);
+    }
     last.D = D;
     last.base = base;
   }

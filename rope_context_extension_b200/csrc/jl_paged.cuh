@@ -60,7 +60,7 @@ struct PagedDecodeArgs {
   int B, Hq, Hkv, r;
   int w0, w_pretrained, qshift;
   float scale_log2;
-  double u_hi[kMaxHalfDim], u_lo[kMaxHalfDim];
+  uint64_t turn[kMaxHalfDim];  // theta_t / 2 pi in 64-bit fixed point
 };
 cudaError_t launch_decode_paged(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedDecodeArgs& a, int D,
                                 cudaStream_t stream);

@@ -21,7 +21,7 @@ int shape_checks(int B, int Hq, int Hkv, int D, double rope_base) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return JL_ERR_INVALID_ARG;
   if (!(rope_base > 0.0) || !std::isfinite(rope_base)) return JL_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return JL_ERR_UNSUPPORTED;
-  if (B > kMaxBatch || Hkv > kMaxBatch || Hq > (1 << 20) || (int64_t)B * Hkv > INT32_MAX) return JL_ERR_UNSUPPORTED;
+  if (B > kMaxBatch || Hkv > kMaxBatch || Hq > (1 << 20) || (int64_t)B * Hkv > (1 << 30)) return JL_ERR_UNSUPPORTED;
   return JL_OK;
 }
 
@@ -45,8 +45,7 @@ int cache_checks(const jl_paged_kv* c, int Hkv, int D, int64_t max_pages, bool n
   if (c->num_pages > INT32_MAX) return JL_ERR_UNSUPPORTED;
   const int64_t limit = int64_t(1) << 38;  // elements: a tensor map's strides stay below 2^40 bytes
   if (c->page_stride < 1 || c->row_stride < 1 || c->head_stride < 1) return JL_ERR_INVALID_ARG;
-  if (c->page_stride > limit || c->row_stride > limit / 1024 || c->head_stride > limit / 1024 / kMaxBatch)
-    return JL_ERR_UNSUPPORTED;
+  if (c->page_stride > limit || c->row_stride > limit || c->head_stride > limit) return JL_ERR_UNSUPPORTED;
   if (c->page_stride % 8 || c->row_stride % 8 || c->head_stride % 8) return JL_ERR_ALIGNMENT;
   const int64_t rows = (c->page_size - 1) * c->row_stride, heads = (Hkv - 1) * c->head_stride;
   const bool by_row = c->head_stride >= D && c->row_stride >= heads + D;   // a row holds all heads
@@ -69,17 +68,18 @@ jl::PagedView view_of(const jl_paged_kv* c) {
   return v;
 }
 
-// 4-D map over (D, Hkv, page rows, pages) of the cache's strides with a
-// {64, 1, 16, 1} box and 128-byte swizzle: 16 rows of one head of one page.
+// 5-D map over (64 dims, page rows, D / 64, Hkv, pages) of the cache's strides with
+// a {64, 16, D / 64, 1, 1} box and 128-byte swizzle: 16 rows of one head of one page
+// in one copy.
 bool encode_pages(CUtensorMap* map, const void* base, const jl_paged_kv* c, int Hkv, int D) {
   auto fn = jl::encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)c->page_size, (cuuint64_t)c->num_pages};
-  cuuint64_t strides[3] = {(cuuint64_t)c->head_stride * 2, (cuuint64_t)c->row_stride * 2,
+  cuuint64_t dims[5] = {64, (cuuint64_t)c->page_size, (cuuint64_t)(D / 64), (cuuint64_t)Hkv, (cuuint64_t)c->num_pages};
+  cuuint64_t strides[4] = {(cuuint64_t)c->row_stride * 2, 128, (cuuint64_t)c->head_stride * 2,
                            (cuuint64_t)c->page_stride * 2};
-  cuuint32_t box[4] = {64, 1, 16, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+  cuuint32_t box[5] = {64, 16, (cuuint32_t)(D / 64), 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -207,7 +207,7 @@ int decode_paged(const void* q, const jl_paged_kv* cache, const int32_t* block_t
   a.w_pretrained = w_pretrained;
   a.qshift = mode;
   a.scale_log2 = jl::resolve_scale(softmax_scale, D) * 1.4426950408889634f;
-  set_turns(a, D, rope_base);
+  std::memcpy(a.turn, jl::turn_table(D, rope_base).fixed, sizeof(a.turn));
   if (jl::launch_decode_paged(tk, tv, a, D, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return JL_ERR_CUDA;
   return JL_OK;

@@ -225,9 +225,10 @@ def test_decode(lens, Hq, Hkv, D, P, w0, W, base, mode):
 @pytest.mark.parametrize("layout", ["rows", "heads", "interleaved", "beside"])
 def test_decode_ratios_and_layouts(r, layout):
     g = torch.Generator().manual_seed(r)
-    lens, P, Hkv, D = [1200, 77], 32, 3, 128
-    k, v = _pool(g, 60, P, Hkv, D, layout)
-    table = _table(g, lens, P, 60)
+    lens, P, Hkv, D = [1200, 77], (32, 16, 128, 1024)[r % 4], 3, 128
+    n = sum(-(-x // P) for x in lens) + 1
+    k, v = _pool(g, n, P, Hkv, D, layout)
+    table = _table(g, lens, P, n)
     q = _randn(g, 2, Hkv * r, D)
     o, lse = torch.empty_like(q), torch.empty(2, Hkv * r, device=DEV)
     jl.jl_bifocal_decode_paged(q, k, v, table, _i32(lens), o, lse, w0=50, w_pretrained=400, rope_base=1e6,
