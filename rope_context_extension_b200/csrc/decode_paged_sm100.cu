@@ -76,7 +76,7 @@ struct PgCfg {
   static constexpr int kSmem = kEntOff + 32 * kWarps + 1024;
   static constexpr int kWtsOff = kQOff;            // the joins' weights; the query fragments are done with
   static constexpr int kMaxParts = 256;            // parts that one join weighs: CTAs of a device, warps of a CTA
-  static_assert((kMaxR * kMaxParts + 2 * kMaxR) * 4 <= kWarps * kQBytes, "room for the weights");
+  static_assert((2 * kMaxR * kMaxParts + 2 * kMaxR) * 4 <= kWarps * kQBytes, "room for the weights");
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -116,15 +116,15 @@ __device__ __forceinline__ void load_keys(uint32_t tile, int ks, uint32_t (&k)[4
   ldsm_x4((tile ^ ((ks & 3) << 5)) + (ks >> 2) * 2048, k[0], k[1], k[2], k[3]);
 }
 
-// Scratch partial: [r] maxima (log2 units), [r] sums, [r][D] outputs.
+// A partial result: 8 maxima (log2 units), 8 sums, [r][D] outputs.
 struct Partial {
   float* m;
   float* l;
   float* o;
 };
-__device__ __forceinline__ Partial partial_at(float* base, int64_t idx, int r, int D, int64_t stride = 0) {
-  float* p = base + idx * (stride ? stride : decode_partial_floats(r, D));
-  return {p, p + r, p + 2 * r};
+__device__ __forceinline__ Partial partial_at(float* base, int64_t idx, int64_t stride) {
+  float* p = base + idx * stride;
+  return {p, p + kMaxR, p + 2 * kMaxR};
 }
 
 // cos and sin of n turns' worth of theta: turn = theta / 2 pi in 64-bit fixed
@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = a.r;
   const int items = a.B * a.Hkv;
+  const int64_t part_floats = decode_partial_floats(r, D);
 
   const int c4 = lane & 3, hrow = lane >> 2;  // column group and row of the mma fragments
   const int hq = kPack ? (hrow & 3) : hrow;   // query head of that row
@@ -260,6 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int my_it = -1;
     int64_t my_s = 0;
     bool open = valid;
+    if (cur_it < items) {  // usually the item at hand holds the whole batch
+      const int64_t end = cur_s + item_units(a, cur_it);
+      if (wb + k0 >= cur_s && wb + min(k0 + 32, cnt) <= end) {
+        open = false;
+        my_it = cur_it;
+        my_s = cur_s;
+      }
+    }
     while (__any_sync(0xffffffffu, open)) {
       const int i = cur_it + lane;
       int n = i < items ? item_units(a, i) : 0;
@@ -288,6 +297,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur_it += 32;
         cur_s += tot;
         if (cur_it >= items) break;  // cannot happen while lengths stay as they were scanned
+      } else {  // the next batch begins in or behind the last unit's item
+        const int last = min(31, cnt - 1 - k0);
+        cur_it = __shfl_sync(0xffffffffu, my_it, last);
+        cur_s = __shfl_sync(0xffffffffu, my_s, last);
       }
     }
     m_phys = -1;
@@ -454,10 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (began && ends) {
             store_final(item);
           } else if (k < cnt) {  // begun before this warp's range
-            store_partial(partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + warp, r, D));
+            store_partial(partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + warp, part_floats));
             if (lane == 0) ent[2 * warp] = {first, n, item};
           } else {  // ends with the range or runs on; the warp's ring is free for it
-            store_partial(partial_at(reinterpret_cast<float*>(smem), warp, r, D, S * C::kSlot / 4));
+            store_partial(partial_at(reinterpret_cast<float*>(smem), warp, S * C::kSlot / 4));
             if (lane == 0) ent[2 * warp + 1] = {first, n, item};
           }
         }
@@ -688,11 +701,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- join the warps' partials, item by item in unit order.  An item's parts are the
   // tails of neighbouring warps and at most one head, of the warp behind them.
   auto row_of = [&](int it) -> int64_t { return (int64_t)(it / a.Hkv) * a.Hq + (it % a.Hkv) * r; };
-  auto write_result = [&](int64_t row, int idx, float o, float M, float l) {
+  auto write_result = [&](int64_t row, int idx, float4 o, float M, float l) {  // four dims from idx = h D + d on
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    a.o[row * D + idx] = __float2bfloat16_rn(o * inv);
+    *reinterpret_cast<uint2*>(a.o + row * D + idx) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     if (idx % D == 0 && a.lse != nullptr)
       a.lse[row + idx / D] = l == 0.f ? -INFINITY : (M + __log2f(l)) * 0.69314718055994531f;
+  };
+  auto add = [](float4& o, float w, const float4& v) {
+    o.x += w * v.x;
+    o.y += w * v.y;
+    o.z += w * v.z;
+    o.w += w * v.w;
   };
   // A part's weight 2^(m - M): an empty part's sum is 0, and a NaN that left the maximum at -inf goes through.
   auto weight = [](float m, float l, float M) { return m == -INFINITY ? l : ex2_approx(m - M); };
@@ -717,36 +737,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       shared_s[slot] = s;
       shared_n[slot] = ent[e].n;
     }
-    const Partial out = partial_at(a.cta_parts, (int64_t)blockIdx.x * 2 + slot, r, D);
-    const Partial hp = partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + (head < 0 ? 0 : head), r, D);
-    for (int idx = tid; idx < r * D; idx += kThreads) {
+    const Partial out = partial_at(a.cta_parts, (int64_t)blockIdx.x * 2 + slot, part_floats);
+    const Partial hp = partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + (head < 0 ? 0 : head), part_floats);
+    static_assert(kMaxR * D / 4 <= kThreads, "one step of the loop below");
+    for (int idx = 4 * tid; idx < r * D; idx += 4 * kThreads) {
       const int h = idx / D;
       float m[kWarps + 1], l[kWarps + 1], M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const Partial p = partial_at(reinterpret_cast<float*>(smem), w, r, D, S * C::kSlot / 4);
-        const bool in = ent[2 * w + 1].item == it;
+      for (int w = 0; w <= kWarps; ++w) {
+        const Partial p = w < kWarps ? partial_at(reinterpret_cast<float*>(smem), w, S * C::kSlot / 4) : hp;
+        const bool in = w < kWarps ? ent[2 * w + 1].item == it : head >= 0;
         m[w] = in ? p.m[h] : -INFINITY;
         l[w] = in ? p.l[h] : 0.f;
         M = fmaxf(M, m[w]);
       }
-      m[kWarps] = head < 0 ? -INFINITY : hp.m[h];
-      l[kWarps] = head < 0 ? 0.f : hp.l[h];
-      M = fmaxf(M, m[kWarps]);
-      float o = 0.f, lsum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float lsum = 0.f;
 #pragma unroll
       for (int w = 0; w <= kWarps; ++w) {
-        const Partial p = partial_at(reinterpret_cast<float*>(smem), w < kWarps ? w : 0, r, D, S * C::kSlot / 4);
+        const Partial p = w < kWarps ? partial_at(reinterpret_cast<float*>(smem), w, S * C::kSlot / 4) : hp;
         const bool in = w < kWarps ? ent[2 * w + 1].item == it : head >= 0;
         const float wt = weight(m[w], l[w], M);
-        const float v = w < kWarps ? p.o[idx] : (head < 0 ? 0.f : hp.o[idx]);
-        if (in) o += wt * v;  // (a ring that holds no part holds anything)
+        if (in) add(o, wt, *reinterpret_cast<const float4*>(p.o + idx));  // (a ring without a part holds anything)
         lsum += wt * l[w];
       }
       if (whole) {
         write_result(row_of(it), idx, o, M, lsum);
       } else {
-        out.o[idx] = o;
+        *reinterpret_cast<float4*>(out.o + idx) = o;
         if (idx % D == 0) {
           out.m[h] = M;
           out.l[h] = lsum;
@@ -757,7 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- join the CTAs' partials: the item's last ticket does it
   float* wts = reinterpret_cast<float*>(smem + C::kWtsOff);  // [r][kMaxParts]
-  float* tot = wts + kMaxR * C::kMaxParts;                   // [r] maxima, then [r] sums
+  float* part_l = wts + kMaxR * C::kMaxParts;                 // [r][kMaxParts] the parts' sums
+  float* tot = part_l + kMaxR * C::kMaxParts;                 // [r] maxima, then [r] sums
   auto cta_of = [&](int64_t unit) -> int { return (int)(((unit + 1) * N - 1) / U); };
 #pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
@@ -772,20 +791,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     __threadfence();
     const int n = last - first + 1;
     // the item begins inside the first CTA's range (slot 1) and before the others' (slot 0)
-    const int64_t step = 2 * decode_partial_floats(r, D);
+    const int64_t step = 2 * part_floats;
     const float* parts = a.cta_parts + first * step;
     for (int h = warp; h < r; h += kWarps) {  // weights, one warp per head
-      auto ml = [&](int c) { return parts + c * step + (c == 0 ? step / 2 : 0) + h; };
-      float M = -INFINITY;
-      for (int c = lane; c < n; c += 32) M = fmaxf(M, __ldcg(ml(c)));
+      float* w = wts + h * C::kMaxParts;
+      float M = -INFINITY, l = 0.f;
+      for (int c = lane; c < n; c += 32) {
+        const float* ml = parts + c * step + (c == 0 ? part_floats : 0) + h;
+        const float mc = __ldcg(ml), lc = __ldcg(ml + kMaxR);
+        w[c] = mc;
+        part_l[h * C::kMaxParts + c] = lc;
+        M = fmaxf(M, mc);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      float l = 0.f;
       for (int c = lane; c < n; c += 32) {
-        const float mc = __ldcg(ml(c)), lc = __ldcg(ml(c) + r);
-        const float wt = weight(mc, lc, M);
-        wts[h * C::kMaxParts + c] = wt;
-        l += wt * lc;
+        const float lc = part_l[h * C::kMaxParts + c];
+        w[c] = weight(w[c], lc, M);
+        l += w[c] * lc;
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -795,16 +818,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncthreads();
-    for (int idx = tid; idx < r * D; idx += kThreads) {
-      const int h = idx / D;
-      const float* w = wts + h * C::kMaxParts;
-      const float* po = parts + 2 * r + idx;
-      float o = w[0] * __ldcg(po + step / 2);
-#pragma unroll 8
-      for (int c = 1; c < n; ++c) o += w[c] * __ldcg(po + c * step);
-      write_result(row_of(it), idx, o, tot[h], tot[kMaxR + h]);
+    // thread groups take every groups-th part of four dims, then their sums meet in unit order
+    const int cols = r * D / 4, groups = kThreads / cols;
+    const int grp = tid / cols, idx = 4 * (tid - grp * cols);
+    float4* sums = reinterpret_cast<float4*>(smem);  // [groups][cols]; the rings are done with
+    if (grp < groups) {
+      const float* w = wts + (idx / D) * C::kMaxParts;
+      const float* po = parts + 2 * kMaxR + idx;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int c = grp; c < n; c += groups)
+        add(o, w[c], __ldcg(reinterpret_cast<const float4*>(po + c * step + (c == 0 ? part_floats : 0))));
+      sums[grp * cols + idx / 4] = o;
     }
-    __syncthreads();  // wts and tot may be written again
+    __syncthreads();
+    if (grp == 0) {
+      float4 o = sums[idx / 4];
+      for (int i = 1; i < groups; ++i) add(o, 1.f, sums[i * cols + idx / 4]);
+      write_result(row_of(it), idx, o, tot[idx / D], tot[kMaxR + idx / D]);
+    }
+    __syncthreads();  // the shared buffers may be written again
   }
 }
 

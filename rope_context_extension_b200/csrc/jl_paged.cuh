@@ -66,8 +66,8 @@ cudaError_t launch_decode_paged(const CUtensorMap& tm_k, const CUtensorMap& tm_v
                                 cudaStream_t stream);
 int decode_paged_max_ctas();
 int decode_paged_warps();
-// Floats of one partial result: r maxima, r sums, r x D outputs.
-inline __host__ __device__ int64_t decode_partial_floats(int r, int D) { return (int64_t)r * (D + 2); }
+// Floats of one partial result: 8 maxima, 8 sums, r x D outputs.
+inline __host__ __device__ int64_t decode_partial_floats(int r, int D) { return 16 + (int64_t)r * D; }
 
 // Page summaries: the mean of a page's keys, each taken to the page's middle position.
 struct PageSummaryArgs {
