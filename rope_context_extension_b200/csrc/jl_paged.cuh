@@ -90,7 +90,12 @@ struct PageSelectArgs {
   const __nv_bfloat16* summaries;  // [num_pages, Hkv, D]
   const int* block_table;          // [B, max_pages]
   const int* seq_lens;             // [B]
-  float* scores;                   // scratch [B, Hkv, max_pages]
+  float* scores;                   // scratch [B, Hkv, max_pages] fp32 scores
+  float* bounds;                   // scratch [B, Hkv, bound_tiles] |q| |c| bounds of 16 pages each
+  int* amb_pages;                  // scratch [B, Hkv, max_pages] pages that the error bound cannot place
+  float* amb_scores;               // scratch [B, Hkv, max_pages] their fp64 scores, rounded
+  int64_t bound_tiles;
+  int tile_pages;                  // pages per CTA of the score kernel
   int* page_list;                  // [B, Hkv, list_stride]
   int* page_counts;                // [B, Hkv]
   int64_t max_pages, list_stride, num_pages;
@@ -101,7 +106,7 @@ struct PageSelectArgs {
   int* dev_error;
   double u_hi[kMaxHalfDim], u_lo[kMaxHalfDim];
 };
-cudaError_t launch_page_select(const PageSelectArgs& a, int D, cudaStream_t stream);
+cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream);
 
 // cos and sin of n * theta (theta / 2 pi = u_hi + u_lo as sincos_int_angle takes
 // it): whole turns removed exactly in fp64, the rest in fp32.  The remainder, at

@@ -290,9 +290,27 @@ int jl_page_summaries(const jl_paged_kv* cache, const int32_t* block_table, int6
   return JL_OK;
 }
 
+namespace {
+struct SelectLayout {
+  size_t scores, bounds, pages, exact, total;
+  int64_t tiles;
+};
+SelectLayout select_layout(int B, int Hkv, int64_t max_pages) {
+  const size_t rows = (size_t)B * Hkv, each = round_up(rows * max_pages * sizeof(float));
+  SelectLayout lay;
+  lay.tiles = (max_pages + 15) / 16;
+  lay.scores = 0;
+  lay.pages = each;
+  lay.exact = 2 * each;
+  lay.bounds = 3 * each;
+  lay.total = lay.bounds + round_up(rows * lay.tiles * sizeof(float));
+  return lay;
+}
+}  // namespace
+
 size_t jl_select_pages_workspace_bytes(int B, int Hkv, int64_t max_pages) {
   if (B < 1 || Hkv < 1 || max_pages < 1 || max_pages > kMaxLen) return 0;
-  return round_up((size_t)B * Hkv * max_pages * sizeof(float));
+  return select_layout(B, Hkv, max_pages).total;
 }
 
 int jl_select_pages(const void* q, const void* summaries, int64_t num_pages, int page_size,
@@ -324,7 +342,13 @@ int jl_select_pages(const void* q, const void* summaries, int64_t num_pages, int
   a.summaries = reinterpret_cast<const __nv_bfloat16*>(summaries);
   a.block_table = block_table;
   a.seq_lens = seq_lens;
-  a.scores = reinterpret_cast<float*>(workspace);
+  const SelectLayout lay = select_layout(B, Hkv, max_pages);
+  char* ws = reinterpret_cast<char*>(workspace);
+  a.scores = reinterpret_cast<float*>(ws + lay.scores);
+  a.amb_pages = reinterpret_cast<int*>(ws + lay.pages);
+  a.amb_scores = reinterpret_cast<float*>(ws + lay.exact);
+  a.bounds = reinterpret_cast<float*>(ws + lay.bounds);
+  a.bound_tiles = lay.tiles;
   a.page_list = page_list;
   a.page_counts = page_counts;
   a.max_pages = max_pages;

@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kSumThreads = 256;
 constexpr int kScoreThreads = 256;
-constexpr int kScorePages = 16;  // pages per CTA of the score kernel
 constexpr int kSelThreads = 512;
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
@@ -135,88 +134,214 @@ __device__ __forceinline__ PageSpan page_span(const PageSelectArgs& a, int b) {
   return {last + 1, min(a.sink_pages, band), band};
 }
 
-// Scores in 64 bits: products of two bf16 values are exact, the angles are good
-// to 1e-10, and the sum is rounded to fp32 once, so that which page lies above a
-// border does not depend on the order of a sum.  One warp per KV head and page,
-// the factors of a CTA's pages in shared memory.
-template <int D>
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_constant__ PageSelectArgs a) {
-  constexpr int H2 = D / 2;
-  constexpr int kOwn = H2 / 32;
-  __shared__ double2 cs[kScorePages + 1][H2];  // row kScorePages: the queries' own factors
+// ---- scores -----------------------------------------------------------------
+// Which page lies above a border must not depend on the order of a sum, so a score
+// is the fp64 value rounded to fp32.  Forming all of them in fp64 is bound by the
+// fp64 pipe and its conversions (110 us for eight sequences of 2048 pages, against
+// 5 us to read the summaries); instead every page gets an fp32 score with a bound
+// on its error, and only pages that the bound cannot place are scored in fp64.
+//
+// fp32 score of 16 consecutive pages for one KV head, by one warp.  As in the
+// decode, the queries take R(dq - dk(c0)) for the group's first page and page u the
+// rest, dk(c_u) - dk(c0) = floor((rm + u P) / G) - u P with rm = c0 mod G, which
+// takes two values per u: a table of 32 rows per sequence.  A lane scores 4 pages
+// over D/16 pairs for every head, and eight lanes' sums meet in an exchange; slot i
+// of a lane is page 4 kg + (i ^ kx), slot h head h ^ hx, so that what an exchange
+// keeps is always the lower half of the slots.
+//
+// Error of one score, in units of 2^-24 |q| |c|: factors 2 x 4 (2^-23 each, the
+// angle's reduction, the rotation's products and sum), products and a chain of
+// D/8 <= 16 sums, three exchanges and one sum of halves 20: below 40.  kScoreErr
+// takes 64; rounding to fp32 adds less than 1.
+constexpr float kScoreErr = 3.814697265625e-6f;    // 2^-18
+constexpr float kTiny = 8.470329472543003e-22f;    // 2^-70: lengths whose squares underflow
+
+__device__ __forceinline__ void lds2x64(uint32_t addr, uint64_t& a, uint64_t& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+}
+__device__ __forceinline__ uint64_t bf16x2_f2(uint32_t w) { return f2_pack(bf16lo_to_f32(w), bf16hi_to_f32(w)); }
+
+// The larger of two scores; a NaN stays.
+__device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }
+
+// kR: query heads per KV head r, padded to 1, 2, 4 or 8.
+template <int D, int kR>
+__global__ void __launch_bounds__(kScoreThreads, kR == 8 ? 1 : 2)
+    page_score_kernel(const __grid_constant__ PageSelectArgs a) {
+  constexpr int H2 = D / 2, NP = D / 16, NJ = NP / 2;
+  constexpr int kQStep = D == 128 ? 1 : 2, kQH = D == 128 ? kR : (kR + 1) / 2;
+  constexpr int kWarps = kScoreThreads / 32;
+  __shared__ __align__(16) float4 etab[32 * NJ * 8];         // [u + 16 extra][j][lane] (c, c, s, s)
+  __shared__ __align__(16) float4 qbufs[kWarps][kR * NJ * 8];  // [head][j][lane] (x, x, y, y)
   const int b = blockIdx.y;
   const PageSpan sp = page_span(a, b);
-  const int p0 = sp.sink + blockIdx.x * kScorePages;
+  const int p0 = sp.sink + blockIdx.x * a.tile_pages;
   if (p0 >= sp.band) return;
-  const int np = min(kScorePages, sp.band - p0);
+  const int groups = (min(a.tile_pages, sp.band - p0) + 15) / 16;
+  const int P = a.page_size;
   const int L = a.seq_lens[b];
-  const int64_t G = group_size(L, a.w_pretrained);
-  const int64_t dq = query_remote(L - 1, G, query_shift(a.w0, G, a.qshift)) - (L - 1);
-  for (int idx = threadIdx.x; idx < (kScorePages + 1) * H2; idx += kScoreThreads) {
-    const int row = idx / H2, t = idx % H2;
-    const int64_t c = (int64_t)(p0 + row) * a.page_size + a.page_size / 2;
-    const int64_t n = row == kScorePages ? dq : key_remote(c, G) - c;
-    double s, co;
-    sincos_int_angle(n, a.u_hi[t], a.u_lo[t], &s, &co);
-    cs[row][t] = make_double2(co, s);
+  const int G = (int)group_size(L, a.w_pretrained);
+  const int dq = (int)(query_remote(L - 1, G, query_shift(a.w0, G, a.qshift)) - (L - 1));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kg = lane >> 3, pg = lane & 7;
+  const int qt = NP * pg + 2 * (D == 128 ? kg : (kg & 1));  // the pairs whose factors this lane forms
+  const int qj = (D == 128 ? kg : (kg & 1)) * 8 + pg;       // and their place in a buffer's row
+  const int qh0 = D == 128 ? 0 : kg >> 1;
+  double uh[2], ul[2];
+  {
+    const double *hp = a.u_hi, *lp = a.u_lo;  // generic reads: an indexed parameter read serialises
+    asm volatile("" : "+l"(hp), "+l"(lp));
+    uh[0] = hp[qt], uh[1] = hp[qt + 1], ul[0] = lp[qt], ul[1] = lp[qt + 1];
+  }
+  auto factors = [&](int64_t n) {
+    float4 f;
+    sincos_turns(n, uh[0], ul[0], &f.z, &f.x);
+    sincos_turns(n, uh[1], ul[1], &f.w, &f.y);
+    return f;
+  };
+  for (int row = kQStep * warp + qh0; row < 32; row += kQStep * kWarps) {
+    const int u = row & 15;
+    etab[row * (NJ * 8) + qj] = factors(u * P / G + (row >> 4) - u * P);
   }
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int g = warp % a.Hkv; g < a.Hkv; g += kScoreThreads / 32) {
-    const int share = max(1, kScoreThreads / 32 / a.Hkv);  // warps per KV head
-    const int first = a.Hkv >= kScoreThreads / 32 ? 0 : warp / a.Hkv;
-    if (first >= share) break;
-    double qx[8][kOwn], qy[8][kOwn];
+  const int hx = pg & (kR - 1), kx = kR == 8 ? 0 : 2 * (pg >> 2);
+  float4* qbuf = qbufs[warp];
+  const uint32_t qaddr = smem_addr(qbuf) + pg * 16, eaddr = smem_addr(etab) + pg * 16;
+  int rem[4];  // u P mod G of this lane's slots
 #pragma unroll
-    for (int h = 0; h < 8; ++h)
+  for (int i = 0; i < 4; ++i) rem[i] = (4 * kg + (i ^ kx)) * P % G;
+  for (int w = warp; w < groups * a.Hkv; w += kWarps) {
+    const int m = w / a.Hkv, g = w - m * a.Hkv;
+    const int page0 = p0 + 16 * m;
+    const int c0 = page0 * P + P / 2;
+    const int q0 = c0 / G, rm = c0 - q0 * G;
+    // this lane's pages: their summaries and factor rows
+    uint4 xw[4], yw[4];
+    uint32_t ef[4];
 #pragma unroll
-      for (int e = 0; e < kOwn; ++e) {
-        const int t = lane + 32 * e;
-        double x = 0.0, y = 0.0;
-        if (h < a.r) {
-          const __nv_bfloat16* q = a.q + ((int64_t)b * a.Hq + g * a.r + h) * D;
-          x = (double)__bfloat162float(q[t]);
-          y = (double)__bfloat162float(q[t + H2]);
-        }
-        const double2 f = cs[kScorePages][t];
-        qx[h][e] = x * f.x - y * f.y;
-        qy[h][e] = y * f.x + x * f.y;
-      }
-    for (int i = first; i < np; i += share) {
-      const int phys = a.block_table[(int64_t)b * a.max_pages + p0 + i];
-      float best = -INFINITY;
+    for (int i = 0; i < 4; ++i) {
+      const int u = 4 * kg + (i ^ kx);
+      xw[i] = yw[i] = make_uint4(0, 0, 0, 0);
+      const int phys = page0 + u < sp.band ? a.block_table[(int64_t)b * a.max_pages + page0 + u] : -1;
       if (phys >= 0 && phys < a.num_pages) {
-        const __nv_bfloat16* k = a.summaries + ((int64_t)phys * a.Hkv + g) * D;
-        double kx[kOwn], ky[kOwn];
-#pragma unroll
-        for (int e = 0; e < kOwn; ++e) {
-          const int t = lane + 32 * e;
-          const double x = (double)__bfloat162float(k[t]), y = (double)__bfloat162float(k[t + H2]);
-          const double2 f = cs[i][t];
-          kx[e] = x * f.x - y * f.y;
-          ky[e] = y * f.x + x * f.y;
+        const __nv_bfloat16* k = a.summaries + ((int64_t)phys * a.Hkv + g) * D + NP * pg;
+        if constexpr (D == 128) {
+          xw[i] = *reinterpret_cast<const uint4*>(k);
+          yw[i] = *reinterpret_cast<const uint4*>(k + H2);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(k), y = *reinterpret_cast<const uint2*>(k + H2);
+          xw[i].x = x.x, xw[i].y = x.y, yw[i].x = y.x, yw[i].y = y.y;
         }
-        double bd = -INFINITY;
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          if (h >= a.r) break;
-          double s = 0.0;
-#pragma unroll
-          for (int e = 0; e < kOwn; ++e) s += qx[h][e] * kx[e] + qy[h][e] * ky[e];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          bd = s != s || s > bd ? s : bd;  // a NaN stays
-          if (s != s) break;
-        }
-        best = (float)bd;
-      } else if (lane == 0 && a.dev_error) {
-        atomicExch(a.dev_error, kDevBadLength);
       }
-      if (lane == 0) a.scores[((int64_t)b * a.Hkv + g) * a.max_pages + p0 + i] = best;
+      ef[i] = eaddr + (u + (rm + rem[i] >= G ? 16 : 0)) * (NJ * 128);
     }
+    // the head's queries, turned for the group's first page
+    const float4 f = factors(dq - (q0 - c0));
+    float qn = 0.f;  // |q|^2 of the heads this lane turns
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kQH; ++i) {
+      const int h = qh0 + kQStep * i;
+      const __nv_bfloat16* qp = a.q + ((int64_t)b * a.Hq + g * a.r + h) * D + qt;
+      const uint32_t xq = h < a.r ? *reinterpret_cast<const uint32_t*>(qp) : 0u;
+      const uint32_t yq = h < a.r ? *reinterpret_cast<const uint32_t*>(qp + H2) : 0u;
+      const float x0 = bf16lo_to_f32(xq), x1 = bf16hi_to_f32(xq), y0 = bf16lo_to_f32(yq), y1 = bf16hi_to_f32(yq);
+      if (h < kR)
+        qbuf[h * (NJ * 8) + qj] =
+            make_float4(x0 * f.x - y0 * f.z, x1 * f.y - y1 * f.w, y0 * f.x + x0 * f.z, y1 * f.y + x1 * f.w);
+      qn += x0 * x0 + x1 * x1 + y0 * y0 + y1 * y1;  // (all heads together bound each)
+    }
+    __syncwarp();
+    uint64_t acc[4][kR], norm[4];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      uint64_t x[4], y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = bf16x2_f2(j == 0 ? xw[i].x : j == 1 ? xw[i].y : j == 2 ? xw[i].z : xw[i].w);
+        y[i] = bf16x2_f2(j == 0 ? yw[i].x : j == 1 ? yw[i].y : j == 2 ? yw[i].z : yw[i].w);
+        norm[i] = f2_fma(y[i], y[i], j == 0 ? f2_mul(x[i], x[i]) : f2_fma(x[i], x[i], norm[i]));
+        uint64_t c, sn;
+        lds2x64(ef[i] + j * 128, c, sn);
+        const uint64_t xr = f2_sub(f2_mul(x[i], c), f2_mul(y[i], sn));
+        y[i] = f2_fma(x[i], sn, f2_mul(y[i], c));
+        x[i] = xr;
+      }
+#pragma unroll
+      for (int h = 0; h < kR; ++h) {
+        uint64_t qa, qb;
+        lds2x64(qaddr + ((h ^ hx) * NJ + j) * 128, qa, qb);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[i][h] = f2_fma(y[i], qb, j == 0 ? f2_mul(x[i], qa) : f2_fma(x[i], qa, acc[i][h]));
+      }
+    }
+    float v[4][kR], big = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      f2_unpack(norm[i], lo, hi);
+      big = max_nan(lo + hi, big);
+#pragma unroll
+      for (int h = 0; h < kR; ++h) {
+        f2_unpack(acc[i][h], lo, hi);
+        v[i][h] = lo + hi;
+      }
+    }
+    constexpr int kV = kR == 8 ? 4 : 2;
+    if constexpr (kR == 8) {
+#pragma unroll
+      for (int s = 4; s >= 1; s >>= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int h = 0; h < s; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h + s], s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int h = 0; h < kR; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i + 2][h], 4);
+#pragma unroll
+        for (int s = 2; s >= 1; s >>= 1) {
+          if (kR > s) {
+#pragma unroll
+            for (int h = 0; h < s; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h + s], s);
+          } else {
+#pragma unroll
+            for (int h = 0; h < kR; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h], s);
+          }
+        }
+      }
+    }
+    // the best head; heads behind r take no part
+    const int kfirst = kR == 8 ? 4 * kg : 4 * kg + 2 * (pg >> 2);
+    float* out = a.scores + ((int64_t)b * a.Hkv + g) * a.max_pages + page0;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      float t = hx < a.r ? v[i][0] : -INFINITY;
+#pragma unroll
+      for (int s = 1; s < kR; s <<= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, s));
+      const int u = kfirst + i;
+      if (hx == 0 && (kR == 8 || (pg & 3) == 0) && page0 + u < sp.band) {
+        const int phys = a.block_table[(int64_t)b * a.max_pages + page0 + u];
+        const bool ok = phys >= 0 && phys < a.num_pages;
+        if (!ok && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
+        out[u] = ok ? t : -INFINITY;
+      }
+    }
+    // an upper bound of |q| |c| over the group: the sum over lanes of each lane's largest part
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1) big += __shfl_xor_sync(0xffffffffu, big, s);
+    big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 8));
+    big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 16));
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) qn += __shfl_xor_sync(0xffffffffu, qn, s);
+    if (lane == 0) a.bounds[((int64_t)b * a.Hkv + g) * a.bound_tiles + (page0 - sp.sink) / 16] =
+          (sqrtf(qn) + kTiny) * (sqrtf(big) + kTiny);
   }
 }
 
+// ---- selection --------------------------------------------------------------
 // Order-preserving key of a score: larger score, larger key; -0 = +0; NaN above all.
 __device__ __forceinline__ uint32_t score_key(float s) {
   if (s != s) return 0xffffffffu;
@@ -224,40 +349,63 @@ __device__ __forceinline__ uint32_t score_key(float s) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per (KV head, sequence): radix selection of the top_k-th largest score
-// key (four passes of 8 bits over the scores), then one pass in page order that
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int cluster_ld(const int* p, int rank) {  // p's word in CTA `rank` of the cluster
+  uint32_t addr;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// One cluster of CTAs per (KV head, sequence), each CTA with a share of the pages.
+// Radix selection of the top_k-th largest fp32 key (four passes of 8 bits, counts
+// joined over the cluster), then the pages that the score's error bound cannot place
+// are scored in fp64 and selected among themselves, then one pass in page order
 // writes the kept pages.
+template <int D>
 __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_constant__ PageSelectArgs a) {
-  __shared__ int hist[256];
+  constexpr int kWarps = kSelThreads / 32;
+  constexpr int kPer = 8;          // pages of a thread per step of an ordered pass
+  __shared__ int hist[256];        // this CTA's counts, read by the cluster
+  __shared__ int share[2];         // this CTA's running counts, read by the cluster
+  __shared__ int wcount[kWarps];
   __shared__ int bucket, above;
-  __shared__ int wk[kSelThreads / 32], wt[kSelThreads / 32];
-  const int g = blockIdx.x, b = blockIdx.y;
+  __shared__ float wmax[kWarps];
+  const int CL = gridDim.x, rank = blockIdx.x;  // the cluster is the grid's x
+  const int g = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = (int64_t)b * a.Hkv + g;
   const PageSpan sp = page_span(a, b);
   const float* sc = a.scores + row * a.max_pages;
   int* list = a.page_list + row * a.list_stride;
   const int cand = sp.band - sp.sink;
-  if (tid == 0 && a.dev_error && !paged_length_ok(a.seq_lens[b], a.max_pages, a.page_size))
+  if (rank == 0 && tid == 0 && a.dev_error && !paged_length_ok(a.seq_lens[b], a.max_pages, a.page_size))
     atomicExch(a.dev_error, kDevBadLength);
 
-  uint32_t thr = 0;  // pages with a larger key are kept, and the first `ties` with this key
-  int ties = 0;
-  if (cand > a.top_k && a.top_k > 0) {
-    int need = a.top_k;
+  // The need-th largest of n keys (this CTA's share: begin .. end): returns it, and in
+  // `need` how many keys equal to it belong to the largest.
+  auto select = [&](auto key_at, int begin, int end, int& need) -> uint32_t {
+    uint32_t thr = 0;
     for (int shift = 24; shift >= 0; shift -= 8) {
       for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int p = sp.sink + tid; p < sp.band; p += kSelThreads) {
-        const uint32_t key = score_key(sc[p]);
+      for (int p = begin + tid; p < end; p += kSelThreads) {
+        const uint32_t key = key_at(p);
         if (shift == 24 || (key >> (shift + 8)) == (thr >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255u], 1);
       }
       __syncthreads();
+      if (CL > 1) cluster_sync();
       if (warp == 0) {  // the bucket, from the top, that holds the need-th key
         int c[8], sum = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          c[i] = hist[255 - (8 * lane + i)];
+          const int* at = &hist[255 - (8 * lane + i)];
+          c[i] = *at;
+          for (int k = 1; k < CL; ++k) c[i] += cluster_ld(at, (rank + k) % CL);
           sum += c[i];
         }
         int incl = sum;
@@ -281,48 +429,200 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
       __syncthreads();
       thr |= (uint32_t)bucket << shift;
       need -= above;
+      if (CL > 1) cluster_sync();  // the counts have been read
       __syncthreads();
     }
-    ties = need;
-  }
-  const bool all = cand <= a.top_k;
+    return thr;
+  };
+  // Sum of v over the CTAs before this one, and over all; v is the same for every thread.
+  auto before = [&](int v, int which, int& all) {
+    all = v;
+    if (CL == 1) return 0;
+    if (tid == 0) share[which] = v;
+    cluster_sync();
+    int sum = 0;
+    for (int k = 0; k < CL; ++k) {
+      if (k == rank) continue;
+      const int t = cluster_ld(&share[which], k);
+      all += t;
+      if (k < rank) sum += t;
+    }
+    cluster_sync();
+    return sum;
+  };
+  // Sum of v over the CTA's threads before this one, and over all of them.
+  auto scan_of = [&](int v, int& total) {
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    __syncthreads();
+    if (lane == 31) wcount[warp] = incl;
+    __syncthreads();
+    int sum = incl - v;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) sum += wcount[w];
+      total += wcount[w];
+    }
+    return sum;
+  };
 
-  int written = 0, seen = 0;  // kept pages so far, pages with the border key so far
-  for (int base = 0; base < sp.pages; base += kSelThreads) {
-    const int p = base + tid;
-    bool keep = false, tie = false;
-    if (p < sp.pages) {
-      if (p < sp.sink || p >= sp.band || all) {
-        keep = true;
-      } else if (a.top_k > 0) {
-        const uint32_t key = score_key(sc[p]);
-        keep = key > thr;
-        tie = key == thr;
+  const bool all = cand <= a.top_k, some = !all && a.top_k > 0;
+  // this CTA's pages of the whole row, and of the scored ones
+  const int per = (sp.pages + CL - 1) / CL;
+  const int begin = min(sp.pages, rank * per), end = min(sp.pages, begin + per);
+  const int sbegin = max(begin, sp.sink), send = max(sbegin, min(end, sp.band));
+  float lo_edge = 0.f, hi_edge = 0.f;  // scores above hi_edge are kept, below lo_edge are not
+  int kept = 0, amb = 0;               // kept for sure, and between the edges, in this CTA
+  // the pages between the edges, in page order, and later whether each is kept
+  int* amb_page = a.amb_pages + row * a.max_pages + sbegin;
+  float* amb_score = a.amb_scores + row * a.max_pages + sbegin;
+  if (some) {
+    int need = a.top_k;
+    const uint32_t kth = select([&](int p) { return score_key(sc[p]); }, sbegin, send, need);
+    const float T = __uint_as_float((kth & 0x80000000u) ? (kth ^ 0x80000000u) : ~kth);  // (a NaN's key gives a NaN)
+    // twice the largest error bound either side of the border's fp32 score
+    float big = 0.f;
+    const float* bounds = a.bounds + row * a.bound_tiles;
+    for (int i = tid; i < (cand + 15) / 16; i += kSelThreads) big = max_nan(bounds[i], big);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, o));
+    if (lane == 0) wmax[warp] = big;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) big = max_nan(wmax[w], big);
+    lo_edge = T - 2.f * kScoreErr * big;  // a NaN or an infinite bound leaves every page between
+    hi_edge = T + 2.f * kScoreErr * big;
+    for (int base = sbegin; base < send; base += kPer * kSelThreads) {
+      const int p0 = base + kPer * tid;
+      unsigned in = 0, up = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (p0 + i >= send) break;
+        const float x = sc[p0 + i];
+        if (x > hi_edge)
+          up |= 1u << i;
+        else if (!(x < lo_edge))
+          in |= 1u << i;
+      }
+      int n;
+      int at = amb + scan_of(__popc(in), n);
+      for (unsigned m = in; m != 0; m &= m - 1) amb_page[at++] = p0 + __ffs(m) - 1;
+      amb += n;
+      scan_of(__popc(up), n);
+      kept += n;
+    }
+    int kept_all, amb_all;
+    before(kept, 0, kept_all);
+    before(amb, 1, amb_all);
+    need = a.top_k - kept_all;
+    __syncthreads();
+    if (need == amb_all) {  // every one of them is kept
+      for (int i = tid; i < amb; i += kSelThreads) amb_score[i] = 1.f;
+      kept += amb;
+    } else {
+      // fp64 scores, one warp per page
+      const int L = a.seq_lens[b];
+      const int64_t G = group_size(L, a.w_pretrained);
+      const int64_t dq = query_remote(L - 1, G, query_shift(a.w0, G, a.qshift)) - (L - 1);
+      for (int i = warp; i < amb; i += kWarps) {
+        const int p = amb_page[i];
+        const int phys = a.block_table[(int64_t)b * a.max_pages + p];
+        const int64_t c = (int64_t)p * a.page_size + a.page_size / 2;
+        double best = -INFINITY;
+        if (phys >= 0 && phys < a.num_pages) {
+          double kx[D / 64], ky[D / 64];  // the summary, turned by all of dk(c) - dq
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e) {
+            const int t = lane + 32 * e;
+            double s, co;
+            sincos_int_angle(key_remote(c, G) - c - dq, a.u_hi[t], a.u_lo[t], &s, &co);
+            const __nv_bfloat16* k = a.summaries + ((int64_t)phys * a.Hkv + g) * D + t;
+            const double x = (double)__bfloat162float(k[0]), y = (double)__bfloat162float(k[D / 2]);
+            kx[e] = x * co - y * s;
+            ky[e] = y * co + x * s;
+          }
+          for (int h = 0; h < a.r; ++h) {
+            const __nv_bfloat16* q = a.q + ((int64_t)b * a.Hq + g * a.r + h) * D;
+            double s = 0.0;
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) {
+              const int t = lane + 32 * e;
+              s += (double)__bfloat162float(q[t]) * kx[e] + (double)__bfloat162float(q[t + D / 2]) * ky[e];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (s > best || s != s) best = s;
+            if (s != s) break;
+          }
+        }
+        if (lane == 0) amb_score[i] = (float)best;
+      }
+      __syncthreads();
+      const uint32_t thr = select([&](int i) { return score_key(amb_score[i]); }, 0, amb, need);
+      // larger keys are kept, and of the equal ones the first `need` in page order
+      int ties = 0;
+      for (int i = tid; i < amb; i += kSelThreads) ties += score_key(amb_score[i]) == thr;
+      int n, tie_all;
+      scan_of(ties, n);
+      int seen = before(n, 0, tie_all);
+      for (int base = 0; base < amb; base += kSelThreads) {
+        const int i = base + tid;
+        const uint32_t key = i < amb ? score_key(amb_score[i]) : 0u;
+        const bool tie = i < amb && key == thr;
+        const int at = seen + scan_of(tie, n);
+        seen += n;
+        const bool keep = i < amb && (key > thr || (tie && at < need));
+        if (i < amb) amb_score[i] = keep ? 1.f : 0.f;
+        scan_of(keep, n);
+        kept += n;
       }
     }
-    const unsigned tb = __ballot_sync(0xffffffffu, tie);
-    if (lane == 0) wt[warp] = __popc(tb);
     __syncthreads();
-    int trank = seen + __popc(tb & ((1u << lane) - 1u)), tall = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < warp) trank += wt[w];
-      tall += wt[w];
-    }
-    seen += tall;
-    keep = keep || (tie && trank < ties);
-    const unsigned kb = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) wk[warp] = __popc(kb);
-    __syncthreads();
-    int at = written + __popc(kb & ((1u << lane) - 1u)), kall = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < warp) at += wk[w];
-      kall += wk[w];
-    }
-    if (keep && at < a.list_stride) list[at] = p;
-    written += kall;
   }
-  for (int64_t i = written + tid; i < a.list_stride; i += kSelThreads) list[i] = -1;
-  if (tid == 0) a.page_counts[row] = written;
+
+  // The kept pages, in page order, behind those of the CTAs before.
+  const int open = all ? max(0, send - sbegin) : kept;
+  const int mine = max(0, min(end, sp.sink) - begin) + open + max(0, end - max(begin, sp.band));
+  int total;
+  int written = before(mine, 0, total), run = 0;
+  for (int base = begin; base < end; base += kPer * kSelThreads) {
+    const int p0 = base + kPer * tid;
+    unsigned keep = 0, in = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int p = p0 + i;
+      if (p >= end) break;
+      if (p < sp.sink || p >= sp.band || all) {
+        keep |= 1u << i;
+      } else if (some) {
+        const float x = sc[p];
+        if (x > hi_edge)
+          keep |= 1u << i;
+        else if (!(x < lo_edge))
+          in |= 1u << i;
+      }
+    }
+    int n;
+    if (some) {
+      int at = run + scan_of(__popc(in), n);
+      run += n;
+      for (unsigned m = in; m != 0; m &= m - 1)
+        if (amb_score[at++] != 0.f) keep |= m & (0u - m);
+    }
+    int at = written + scan_of(__popc(keep), n);
+    written += n;
+    for (unsigned m = keep; m != 0; m &= m - 1, ++at)
+      if (at < a.list_stride) list[at] = p0 + __ffs(m) - 1;
+  }
+  if (rank == CL - 1) {
+    for (int64_t i = total + tid; i < a.list_stride; i += kSelThreads) list[i] = -1;
+    if (tid == 0) a.page_counts[row] = total;
+  }
 }
 
 template <int D>
@@ -346,18 +646,54 @@ cudaError_t launch_page_summaries(const PageSummaryArgs& a, int D, cudaStream_t 
   return D == 128 ? launch_summary_d<128>(a, stream) : launch_summary_d<64>(a, stream);
 }
 
-cudaError_t launch_page_select(const PageSelectArgs& a, int D, cudaStream_t stream) {
-  const dim3 grid((unsigned)((a.max_pages + kScorePages - 1) / kScorePages), a.B);
+namespace {
+
+template <int D>
+cudaError_t launch_score_d(const PageSelectArgs& a, cudaStream_t stream) {
+  const dim3 grid((unsigned)((a.max_pages + a.tile_pages - 1) / a.tile_pages), a.B);
+  if (a.r == 1)
+    page_score_kernel<D, 1><<<grid, kScoreThreads, 0, stream>>>(a);
+  else if (a.r == 2)
+    page_score_kernel<D, 2><<<grid, kScoreThreads, 0, stream>>>(a);
+  else if (a.r <= 4)
+    page_score_kernel<D, 4><<<grid, kScoreThreads, 0, stream>>>(a);
+  else
+    page_score_kernel<D, 8><<<grid, kScoreThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream) {
+  cudaError_t e;
   if (a.top_k > 0) {
-    if (D == 128)
-      page_score_kernel<128><<<grid, kScoreThreads, 0, stream>>>(a);
-    else
-      page_score_kernel<64><<<grid, kScoreThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    // Tiles of up to 128 pages share a factor table; smaller ones while the tiles do
+    // not fill the GPU (two CTAs per SM).
+    int dev = 0, sms = 148;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    a.tile_pages = 128;
+    while (a.tile_pages > 16 && (a.max_pages + a.tile_pages - 1) / a.tile_pages * a.B < 2 * sms) a.tile_pages /= 2;
+    e = D == 128 ? launch_score_d<128>(a, stream) : launch_score_d<64>(a, stream);
     if (e != cudaSuccess) return e;
   }
-  page_select_kernel<<<dim3(a.Hkv, a.B), kSelThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  // One CTA per 4096 pages, at most eight (the portable cluster size).
+  int cl = 1;
+  while (cl < 8 && (int64_t)cl * 4096 < a.max_pages) cl *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cl, a.Hkv, a.B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cl;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const PageSelectArgs& ca = a;
+  return D == 128 ? cudaLaunchKernelEx(&cfg, page_select_kernel<128>, ca)
+                  : cudaLaunchKernelEx(&cfg, page_select_kernel<64>, ca);
 }
 
 }  // namespace jl
