@@ -105,6 +105,7 @@ struct PageSelectArgs {
   int sink_pages, top_k;
   int* dev_error;
   double u_hi[kMaxHalfDim], u_lo[kMaxHalfDim];
+  uint64_t turn[kMaxHalfDim];      // theta_t / 2 pi in 64-bit fixed point
 };
 cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream);
 

@@ -366,6 +366,7 @@ int jl_select_pages(const void* q, const void* summaries, int64_t num_pages, int
   a.top_k = top_k;
   a.dev_error = dev_error;
   set_turns(a, head_dim, rope_base);
+  std::memcpy(a.turn, jl::turn_table(head_dim, rope_base).fixed, sizeof(a.turn));
   if (jl::launch_page_select(a, head_dim, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return JL_ERR_CUDA;
   return JL_OK;
 }

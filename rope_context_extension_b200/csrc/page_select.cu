@@ -22,8 +22,9 @@ namespace jl {
 namespace {
 
 constexpr int kSumThreads = 256;
-constexpr int kScoreThreads = 256;
+constexpr int kMaxTile = 128;       // pages per CTA of the score kernel, at most
 constexpr int kSelThreads = 512;
+constexpr int kRank = 128;          // pages between the edges that are ranked by comparing all
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -161,18 +162,31 @@ __device__ __forceinline__ void lds2x64(uint32_t addr, uint64_t& a, uint64_t& b)
 }
 __device__ __forceinline__ uint64_t bf16x2_f2(uint32_t w) { return f2_pack(bf16lo_to_f32(w), bf16hi_to_f32(w)); }
 
+// cos and sin of n theta, theta / 2 pi in 64-bit fixed point (whole turns fall off
+// the top): the phase is good to 2^-31 turns plus n 2^-56, the rest to fp32.
+__device__ __forceinline__ void sincos_fixed(int n, uint64_t turn, float* s, float* c) {
+  const uint32_t m = (uint32_t)(n < 0 ? -n : n);
+  const uint32_t ph = m * (uint32_t)(turn >> 32) + __umulhi(m, (uint32_t)turn);
+  float sn;
+  sincospif((float)(int32_t)ph * 4.656612873077393e-10f, &sn, c);  // 2 / 2^32
+  *s = n < 0 ? -sn : sn;
+}
+
 // The larger of two scores; a NaN stays.
 __device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }
 
+__host__ __device__ constexpr int score_threads(int kR) { return kR == 8 ? 128 : 256; }  // eight heads' sums: twice the registers
+
 // kR: query heads per KV head r, padded to 1, 2, 4 or 8.
 template <int D, int kR>
-__global__ void __launch_bounds__(kScoreThreads, kR == 8 ? 1 : 2)
+__global__ void __launch_bounds__(score_threads(kR), 2)
     page_score_kernel(const __grid_constant__ PageSelectArgs a) {
   constexpr int H2 = D / 2, NP = D / 16, NJ = NP / 2;
   constexpr int kQStep = D == 128 ? 1 : 2, kQH = D == 128 ? kR : (kR + 1) / 2;
-  constexpr int kWarps = kScoreThreads / 32;
+  constexpr int kThreads = score_threads(kR), kWarps = kThreads / 32;
   __shared__ __align__(16) float4 etab[32 * NJ * 8];         // [u + 16 extra][j][lane] (c, c, s, s)
   __shared__ __align__(16) float4 qbufs[kWarps][kR * NJ * 8];  // [head][j][lane] (x, x, y, y)
+  __shared__ int pages[kMaxTile];                            // the tile's pages in the pool, -1: none
   const int b = blockIdx.y;
   const PageSpan sp = page_span(a, b);
   const int p0 = sp.sink + blockIdx.x * a.tile_pages;
@@ -187,18 +201,25 @@ __global__ void __launch_bounds__(kScoreThreads, kR == 8 ? 1 : 2)
   const int qt = NP * pg + 2 * (D == 128 ? kg : (kg & 1));  // the pairs whose factors this lane forms
   const int qj = (D == 128 ? kg : (kg & 1)) * 8 + pg;       // and their place in a buffer's row
   const int qh0 = D == 128 ? 0 : kg >> 1;
-  double uh[2], ul[2];
+  uint64_t turn0, turn1;
   {
-    const double *hp = a.u_hi, *lp = a.u_lo;  // generic reads: an indexed parameter read serialises
-    asm volatile("" : "+l"(hp), "+l"(lp));
-    uh[0] = hp[qt], uh[1] = hp[qt + 1], ul[0] = lp[qt], ul[1] = lp[qt + 1];
+    const uint64_t* tp = a.turn;  // a generic read: an indexed parameter read serialises
+    asm volatile("" : "+l"(tp));
+    turn0 = tp[qt];
+    turn1 = tp[qt + 1];
   }
-  auto factors = [&](int64_t n) {
+  auto factors = [&](int n) {
     float4 f;
-    sincos_turns(n, uh[0], ul[0], &f.z, &f.x);
-    sincos_turns(n, uh[1], ul[1], &f.w, &f.y);
+    sincos_fixed(n, turn0, &f.z, &f.x);
+    sincos_fixed(n, turn1, &f.w, &f.y);
     return f;
   };
+  for (int i = threadIdx.x; i < 16 * groups; i += kThreads) {
+    const int phys = p0 + i < sp.band ? a.block_table[(int64_t)b * a.max_pages + p0 + i] : -1;
+    const bool ok = phys >= 0 && phys < a.num_pages;
+    if (!ok && p0 + i < sp.band && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
+    pages[i] = ok ? phys : -1;
+  }
   for (int row = kQStep * warp + qh0; row < 32; row += kQStep * kWarps) {
     const int u = row & 15;
     etab[row * (NJ * 8) + qj] = factors(u * P / G + (row >> 4) - u * P);
@@ -222,8 +243,8 @@ __global__ void __launch_bounds__(kScoreThreads, kR == 8 ? 1 : 2)
     for (int i = 0; i < 4; ++i) {
       const int u = 4 * kg + (i ^ kx);
       xw[i] = yw[i] = make_uint4(0, 0, 0, 0);
-      const int phys = page0 + u < sp.band ? a.block_table[(int64_t)b * a.max_pages + page0 + u] : -1;
-      if (phys >= 0 && phys < a.num_pages) {
+      const int phys = pages[16 * m + u];
+      if (phys >= 0) {
         const __nv_bfloat16* k = a.summaries + ((int64_t)phys * a.Hkv + g) * D + NP * pg;
         if constexpr (D == 128) {
           xw[i] = *reinterpret_cast<const uint4*>(k);
@@ -322,12 +343,8 @@ __global__ void __launch_bounds__(kScoreThreads, kR == 8 ? 1 : 2)
 #pragma unroll
       for (int s = 1; s < kR; s <<= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, s));
       const int u = kfirst + i;
-      if (hx == 0 && (kR == 8 || (pg & 3) == 0) && page0 + u < sp.band) {
-        const int phys = a.block_table[(int64_t)b * a.max_pages + page0 + u];
-        const bool ok = phys >= 0 && phys < a.num_pages;
-        if (!ok && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
-        out[u] = ok ? t : -INFINITY;
-      }
+      if (hx == 0 && (kR == 8 || (pg & 3) == 0) && page0 + u < sp.band)
+        out[u] = pages[16 * m + u] >= 0 ? t : -INFINITY;
     }
     // an upper bound of |q| |c| over the group: the sum over lanes of each lane's largest part
 #pragma unroll
@@ -361,6 +378,12 @@ __device__ __forceinline__ int cluster_ld(const int* p, int rank) {  // p's word
   return v;
 }
 
+__device__ __forceinline__ void cluster_st(uint32_t* p, int rank, uint32_t v) {
+  uint32_t addr;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // One cluster of CTAs per (KV head, sequence), each CTA with a share of the pages.
 // Radix selection of the top_k-th largest fp32 key (four passes of 8 bits, counts
 // joined over the cluster), then the pages that the score's error bound cannot place
@@ -373,7 +396,8 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
   __shared__ int hist[256];        // this CTA's counts, read by the cluster
   __shared__ int share[2];         // this CTA's running counts, read by the cluster
   __shared__ int wcount[kWarps];
-  __shared__ int bucket, above;
+  __shared__ int found[3];         // bucket, keys above it, keys in it
+  __shared__ uint32_t rkey[kRank];
   __shared__ float wmax[kWarps];
   const int CL = gridDim.x, rank = blockIdx.x;  // the cluster is the grid's x
   const int g = blockIdx.y, b = blockIdx.z;
@@ -386,26 +410,39 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
   if (rank == 0 && tid == 0 && a.dev_error && !paged_length_ok(a.seq_lens[b], a.max_pages, a.page_size))
     atomicExch(a.dev_error, kDevBadLength);
 
-  // The need-th largest of n keys (this CTA's share: begin .. end): returns it, and in
-  // `need` how many keys equal to it belong to the largest.
-  auto select = [&](auto key_at, int begin, int end, int& need) -> uint32_t {
-    uint32_t thr = 0;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+  // Radix search for the need-th largest key (this CTA's share: begin .. end), 8 bits at a
+  // time: thr gets its upper bits, `need` the number of keys among those with the same upper
+  // bits that belong to the largest.  Stops short of the low bits, whose number it returns,
+  // after two passes or more once at most `few` keys share the upper ones.
+  uint32_t thr = 0;
+  auto select = [&](auto key_at, int begin, int end, int& need, int few) -> int {
+    thr = 0;
+    int shift = 32, in_bucket = 0;
+    do {
+      shift -= 8;
+      if (tid < 256) hist[tid] = 0;
       __syncthreads();
       for (int p = begin + tid; p < end; p += kSelThreads) {
         const uint32_t key = key_at(p);
         if (shift == 24 || (key >> (shift + 8)) == (thr >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255u], 1);
       }
       __syncthreads();
-      if (CL > 1) cluster_sync();
+      if (CL > 1) {
+        cluster_sync();
+        int sum = 0;
+        if (tid < 256) {
+          sum = hist[tid];
+          for (int k = 1; k < CL; ++k) sum += cluster_ld(&hist[tid], (rank + k) % CL);
+        }
+        cluster_sync();  // every CTA has read the others' counts
+        if (tid < 256) hist[tid] = sum;
+        __syncthreads();
+      }
       if (warp == 0) {  // the bucket, from the top, that holds the need-th key
         int c[8], sum = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int* at = &hist[255 - (8 * lane + i)];
-          c[i] = *at;
-          for (int k = 1; k < CL; ++k) c[i] += cluster_ld(at, (rank + k) % CL);
+          c[i] = hist[255 - (8 * lane + i)];
           sum += c[i];
         }
         int incl = sum;
@@ -419,20 +456,21 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (run < need && need <= run + c[i]) {
-              bucket = 255 - (8 * lane + i);
-              above = run;
+              found[0] = 255 - (8 * lane + i);
+              found[1] = run;
+              found[2] = c[i];
             }
             run += c[i];
           }
         }
       }
       __syncthreads();
-      thr |= (uint32_t)bucket << shift;
-      need -= above;
-      if (CL > 1) cluster_sync();  // the counts have been read
+      thr |= (uint32_t)found[0] << shift;
+      need -= found[1];
+      in_bucket = found[2];
       __syncthreads();
-    }
-    return thr;
+    } while (shift > 0 && (shift > 16 || in_bucket > few));
+    return shift;
   };
   // Sum of v over the CTAs before this one, and over all; v is the same for every thread.
   auto before = [&](int v, int which, int& all) {
@@ -483,9 +521,11 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
   float* amb_score = a.amb_scores + row * a.max_pages + sbegin;
   if (some) {
     int need = a.top_k;
-    const uint32_t kth = select([&](int p) { return score_key(sc[p]); }, sbegin, send, need);
-    const float T = __uint_as_float((kth & 0x80000000u) ? (kth ^ 0x80000000u) : ~kth);  // (a NaN's key gives a NaN)
-    // twice the largest error bound either side of the border's fp32 score
+    const int low = select([&](int p) { return score_key(sc[p]); }, sbegin, send, need, kRank / 2);
+    // The border's fp32 score lies between these two (a NaN's key gives a NaN).
+    auto score_of = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k); };
+    const float T0 = score_of(thr), T1 = score_of(thr | ((1u << low) - 1u));
+    // twice the largest error bound beyond them either side
     float big = 0.f;
     const float* bounds = a.bounds + row * a.bound_tiles;
     for (int i = tid; i < (cand + 15) / 16; i += kSelThreads) big = max_nan(bounds[i], big);
@@ -495,8 +535,8 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) big = max_nan(wmax[w], big);
-    lo_edge = T - 2.f * kScoreErr * big;  // a NaN or an infinite bound leaves every page between
-    hi_edge = T + 2.f * kScoreErr * big;
+    lo_edge = T0 - 2.f * kScoreErr * big;  // a NaN or an infinite bound leaves every page between
+    hi_edge = T1 + 2.f * kScoreErr * big;
     for (int base = sbegin; base < send; base += kPer * kSelThreads) {
       const int p0 = base + kPer * tid;
       unsigned in = 0, up = 0;
@@ -518,7 +558,7 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
     }
     int kept_all, amb_all;
     before(kept, 0, kept_all);
-    before(amb, 1, amb_all);
+    const int amb_first = before(amb, 1, amb_all);
     need = a.top_k - kept_all;
     __syncthreads();
     if (need == amb_all) {  // every one of them is kept
@@ -563,23 +603,41 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
         if (lane == 0) amb_score[i] = (float)best;
       }
       __syncthreads();
-      const uint32_t thr = select([&](int i) { return score_key(amb_score[i]); }, 0, amb, need);
-      // larger keys are kept, and of the equal ones the first `need` in page order
-      int ties = 0;
-      for (int i = tid; i < amb; i += kSelThreads) ties += score_key(amb_score[i]) == thr;
-      int n, tie_all;
-      scan_of(ties, n);
-      int seen = before(n, 0, tie_all);
-      for (int base = 0; base < amb; base += kSelThreads) {
-        const int i = base + tid;
-        const uint32_t key = i < amb ? score_key(amb_score[i]) : 0u;
-        const bool tie = i < amb && key == thr;
-        const int at = seen + scan_of(tie, n);
-        seen += n;
-        const bool keep = i < amb && (key > thr || (tie && at < need));
-        if (i < amb) amb_score[i] = keep ? 1.f : 0.f;
-        scan_of(keep, n);
-        kept += n;
+      if (amb_all <= kRank) {  // every CTA of the cluster gets all keys and ranks its own
+        for (int i = tid; i < amb; i += kSelThreads)
+          for (int k = 0; k < CL; ++k) cluster_st(&rkey[amb_first + i], k, score_key(amb_score[i]));
+        if (CL > 1)
+          cluster_sync();
+        else
+          __syncthreads();
+        bool keep = false;
+        if (tid < amb) {
+          const int me = amb_first + tid;
+          int better = 0;
+          for (int i = 0; i < amb_all; ++i) better += rkey[i] > rkey[me] || (rkey[i] == rkey[me] && i < me);
+          keep = better < need;
+          amb_score[tid] = keep ? 1.f : 0.f;
+        }
+        kept += __syncthreads_count(keep);
+      } else {
+        select([&](int i) { return score_key(amb_score[i]); }, 0, amb, need, 0);
+        // larger keys are kept, and of the equal ones the first `need` in page order
+        int ties = 0;
+        for (int i = tid; i < amb; i += kSelThreads) ties += score_key(amb_score[i]) == thr;
+        int n, tie_all;
+        scan_of(ties, n);
+        int seen = before(n, 0, tie_all);
+        for (int base = 0; base < amb; base += kSelThreads) {
+          const int i = base + tid;
+          const uint32_t key = i < amb ? score_key(amb_score[i]) : 0u;
+          const bool tie = i < amb && key == thr;
+          const int at = seen + scan_of(tie, n);
+          seen += n;
+          const bool keep = i < amb && (key > thr || (tie && at < need));
+          if (i < amb) amb_score[i] = keep ? 1.f : 0.f;
+          scan_of(keep, n);
+          kept += n;
+        }
       }
     }
     __syncthreads();
@@ -652,13 +710,13 @@ template <int D>
 cudaError_t launch_score_d(const PageSelectArgs& a, cudaStream_t stream) {
   const dim3 grid((unsigned)((a.max_pages + a.tile_pages - 1) / a.tile_pages), a.B);
   if (a.r == 1)
-    page_score_kernel<D, 1><<<grid, kScoreThreads, 0, stream>>>(a);
+    page_score_kernel<D, 1><<<grid, score_threads(1), 0, stream>>>(a);
   else if (a.r == 2)
-    page_score_kernel<D, 2><<<grid, kScoreThreads, 0, stream>>>(a);
+    page_score_kernel<D, 2><<<grid, score_threads(2), 0, stream>>>(a);
   else if (a.r <= 4)
-    page_score_kernel<D, 4><<<grid, kScoreThreads, 0, stream>>>(a);
+    page_score_kernel<D, 4><<<grid, score_threads(4), 0, stream>>>(a);
   else
-    page_score_kernel<D, 8><<<grid, kScoreThreads, 0, stream>>>(a);
+    page_score_kernel<D, 8><<<grid, score_threads(8), 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -672,7 +730,7 @@ cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream) {
     int dev = 0, sms = 148;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    a.tile_pages = 128;
+    a.tile_pages = kMaxTile;
     while (a.tile_pages > 16 && (a.max_pages + a.tile_pages - 1) / a.tile_pages * a.B < 2 * sms) a.tile_pages /= 2;
     e = D == 128 ? launch_score_d<128>(a, stream) : launch_score_d<64>(a, stream);
     if (e != cudaSuccess) return e;
