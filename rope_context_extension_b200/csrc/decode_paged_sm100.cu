@@ -127,19 +127,6 @@ __device__ __forceinline__ Partial partial_at(float* base, int64_t idx, int64_t 
   return {p, p + kMaxR, p + 2 * kMaxR};
 }
 
-// cos and sin of n turns' worth of theta: turn = theta / 2 pi in 64-bit fixed
-// point, whole turns fall off the top.  The phase is good to 2^-31 turns plus
-// n 2^-56, the MUFU's sine and cosine to 2^-21 (their documented bound in
-// [-pi, pi]), which puts 2^-21 |q| |k| on a score.
-__device__ __forceinline__ void sincos_phase(int n, uint64_t turn, float* s, float* c) {
-  const uint32_t m = (uint32_t)(n < 0 ? -n : n);
-  const uint32_t ph = m * (uint32_t)(turn >> 32) + __umulhi(m, (uint32_t)turn);
-  const float x = (float)(int32_t)ph * 1.4629180792671596e-9f;  // 2 pi / 2^32
-  const float sn = __sinf(x);
-  *s = n < 0 ? -sn : sn;
-  *c = __cosf(x);
-}
-
 // kPack: at most four query heads per KV head, duplicated in M rows 4-7 so that
 // those rows' lanes carry the probabilities' lo parts.
 template <int D, bool kPack>

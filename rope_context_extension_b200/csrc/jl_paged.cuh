@@ -121,6 +121,19 @@ __device__ __forceinline__ void sincos_turns(int64_t n, double u_hi, double u_lo
   sincospif(2.f * (float)f, s, c);
 }
 
+// cos and sin of n turns' worth of theta: turn = theta / 2 pi in 64-bit fixed
+// point, whole turns fall off the top.  The phase is good to 2^-31 turns plus
+// n 2^-56, the MUFU's sine and cosine to 2^-21 (their documented bound in
+// [-pi, pi]), which puts 2^-21 |q| |k| on a score.
+__device__ __forceinline__ void sincos_phase(int n, uint64_t turn, float* s, float* c) {
+  const uint32_t m = (uint32_t)(n < 0 ? -n : n);
+  const uint32_t ph = m * (uint32_t)(turn >> 32) + __umulhi(m, (uint32_t)turn);
+  const float x = (float)(int32_t)ph * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float sn = __sinf(x);
+  *s = n < 0 ? -sn : sn;
+  *c = __cosf(x);
+}
+
 // A sequence's length as the paged operators take it: 0 .. max_pages * page_size,
 // anything else counts as empty (the caller flags kDevBadLength).
 __device__ __forceinline__ bool paged_length_ok(int L, int64_t max_pages, int page_size) {

@@ -150,10 +150,10 @@ __device__ __forceinline__ PageSpan page_span(const PageSelectArgs& a, int b) {
 // of a lane is page 4 kg + (i ^ kx), slot h head h ^ hx, so that what an exchange
 // keeps is always the lower half of the slots.
 //
-// Error of one score, in units of 2^-24 |q| |c|: factors 2 x 4 (2^-23 each, the
-// angle's reduction, the rotation's products and sum), products and a chain of
-// D/8 <= 16 sums, three exchanges and one sum of halves 20: below 40.  kScoreErr
-// takes 64; rounding to fp32 adds less than 1.
+// Error of one score, in units of 2^-24 |q| |c|: the table's factors and the keys'
+// rotation 4, the queries' factors (the MUFU's 2^-21.2 each) and rotation 12, a chain
+// of eight fused sums, the sum of halves and three exchanges 12, the rounding to fp32
+// 1: below 30.  kScoreErr takes 64.
 constexpr float kScoreErr = 3.814697265625e-6f;    // 2^-18
 constexpr float kTiny = 8.470329472543003e-22f;    // 2^-70: lengths whose squares underflow
 
@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(score_threads(kR), 2)
   }
   auto factors = [&](int n) {
     float4 f;
-    sincos_fixed(n, turn0, &f.z, &f.x);
-    sincos_fixed(n, turn1, &f.w, &f.y);
+    sincos_phase(n, turn0, &f.z, &f.x);
+    sincos_phase(n, turn1, &f.w, &f.y);
     return f;
   };
   for (int i = threadIdx.x; i < 16 * groups; i += kThreads) {
@@ -222,7 +222,11 @@ __global__ void __launch_bounds__(score_threads(kR), 2)
   }
   for (int row = kQStep * warp + qh0; row < 32; row += kQStep * kWarps) {
     const int u = row & 15;
-    etab[row * (NJ * 8) + qj] = factors(u * P / G + (row >> 4) - u * P);
+    const int n = u * P / G + (row >> 4) - u * P;
+    float4 f;
+    sincos_fixed(n, turn0, &f.z, &f.x);
+    sincos_fixed(n, turn1, &f.w, &f.y);
+    etab[row * (NJ * 8) + qj] = f;
   }
   __syncthreads();
   const int hx = pg & (kR - 1), kx = kR == 8 ? 0 : 2 * (pg >> 2);
@@ -231,130 +235,138 @@ __global__ void __launch_bounds__(score_threads(kR), 2)
   int rem[4];  // u P mod G of this lane's slots
 #pragma unroll
   for (int i = 0; i < 4; ++i) rem[i] = (4 * kg + (i ^ kx)) * P % G;
-  for (int w = warp; w < groups * a.Hkv; w += kWarps) {
-    const int m = w / a.Hkv, g = w - m * a.Hkv;
+  // A warp takes a group of 16 pages and a share of the KV heads: what depends on the
+  // positions alone is formed once for them.
+  const int shares = max(1, min(a.Hkv, kWarps / groups)), per = (a.Hkv + shares - 1) / shares;
+  for (int w = warp; w < groups * shares; w += kWarps) {
+    const int m = w / shares, g0 = (w - m * shares) * per, g1 = min(a.Hkv, g0 + per);
     const int page0 = p0 + 16 * m;
     const int c0 = page0 * P + P / 2;
     const int q0 = c0 / G, rm = c0 - q0 * G;
-    // this lane's pages: their summaries and factor rows
-    uint4 xw[4], yw[4];
+    const float4 f = factors(dq - (q0 - c0));
+    int phys[4];      // this lane's pages and their factor rows
     uint32_t ef[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int u = 4 * kg + (i ^ kx);
-      xw[i] = yw[i] = make_uint4(0, 0, 0, 0);
-      const int phys = pages[16 * m + u];
-      if (phys >= 0) {
-        const __nv_bfloat16* k = a.summaries + ((int64_t)phys * a.Hkv + g) * D + NP * pg;
-        if constexpr (D == 128) {
-          xw[i] = *reinterpret_cast<const uint4*>(k);
-          yw[i] = *reinterpret_cast<const uint4*>(k + H2);
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(k), y = *reinterpret_cast<const uint2*>(k + H2);
-          xw[i].x = x.x, xw[i].y = x.y, yw[i].x = y.x, yw[i].y = y.y;
-        }
-      }
+      phys[i] = pages[16 * m + u];
       ef[i] = eaddr + (u + (rm + rem[i] >= G ? 16 : 0)) * (NJ * 128);
     }
-    // the head's queries, turned for the group's first page
-    const float4 f = factors(dq - (q0 - c0));
-    float qn = 0.f;  // |q|^2 of the heads this lane turns
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kQH; ++i) {
-      const int h = qh0 + kQStep * i;
-      const __nv_bfloat16* qp = a.q + ((int64_t)b * a.Hq + g * a.r + h) * D + qt;
-      const uint32_t xq = h < a.r ? *reinterpret_cast<const uint32_t*>(qp) : 0u;
-      const uint32_t yq = h < a.r ? *reinterpret_cast<const uint32_t*>(qp + H2) : 0u;
-      const float x0 = bf16lo_to_f32(xq), x1 = bf16hi_to_f32(xq), y0 = bf16lo_to_f32(yq), y1 = bf16hi_to_f32(yq);
-      if (h < kR)
-        qbuf[h * (NJ * 8) + qj] =
-            make_float4(x0 * f.x - y0 * f.z, x1 * f.y - y1 * f.w, y0 * f.x + x0 * f.z, y1 * f.y + x1 * f.w);
-      qn += x0 * x0 + x1 * x1 + y0 * y0 + y1 * y1;  // (all heads together bound each)
-    }
-    __syncwarp();
-    uint64_t acc[4][kR], norm[4];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      uint64_t x[4], y[4];
+    for (int g = g0; g < g1; ++g) {
+      uint4 xw[4], yw[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[i] = bf16x2_f2(j == 0 ? xw[i].x : j == 1 ? xw[i].y : j == 2 ? xw[i].z : xw[i].w);
-        y[i] = bf16x2_f2(j == 0 ? yw[i].x : j == 1 ? yw[i].y : j == 2 ? yw[i].z : yw[i].w);
-        norm[i] = f2_fma(y[i], y[i], j == 0 ? f2_mul(x[i], x[i]) : f2_fma(x[i], x[i], norm[i]));
-        uint64_t c, sn;
-        lds2x64(ef[i] + j * 128, c, sn);
-        const uint64_t xr = f2_sub(f2_mul(x[i], c), f2_mul(y[i], sn));
-        y[i] = f2_fma(x[i], sn, f2_mul(y[i], c));
-        x[i] = xr;
-      }
-#pragma unroll
-      for (int h = 0; h < kR; ++h) {
-        uint64_t qa, qb;
-        lds2x64(qaddr + ((h ^ hx) * NJ + j) * 128, qa, qb);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[i][h] = f2_fma(y[i], qb, j == 0 ? f2_mul(x[i], qa) : f2_fma(x[i], qa, acc[i][h]));
-      }
-    }
-    float v[4][kR], big = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float lo, hi;
-      f2_unpack(norm[i], lo, hi);
-      big = max_nan(lo + hi, big);
-#pragma unroll
-      for (int h = 0; h < kR; ++h) {
-        f2_unpack(acc[i][h], lo, hi);
-        v[i][h] = lo + hi;
-      }
-    }
-    constexpr int kV = kR == 8 ? 4 : 2;
-    if constexpr (kR == 8) {
-#pragma unroll
-      for (int s = 4; s >= 1; s >>= 1)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int h = 0; h < s; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h + s], s);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int h = 0; h < kR; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i + 2][h], 4);
-#pragma unroll
-        for (int s = 2; s >= 1; s >>= 1) {
-          if (kR > s) {
-#pragma unroll
-            for (int h = 0; h < s; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h + s], s);
+        xw[i] = yw[i] = make_uint4(0, 0, 0, 0);
+        if (phys[i] >= 0) {
+          const __nv_bfloat16* k = a.summaries + ((int64_t)phys[i] * a.Hkv + g) * D + NP * pg;
+          if constexpr (D == 128) {
+            xw[i] = *reinterpret_cast<const uint4*>(k);
+            yw[i] = *reinterpret_cast<const uint4*>(k + H2);
           } else {
-#pragma unroll
-            for (int h = 0; h < kR; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h], s);
+            const uint2 x = *reinterpret_cast<const uint2*>(k), y = *reinterpret_cast<const uint2*>(k + H2);
+            xw[i].x = x.x, xw[i].y = x.y, yw[i].x = y.x, yw[i].y = y.y;
           }
         }
       }
+      // the head's queries, turned for the group's first page
+      float qn = 0.f;  // |q|^2 of the heads this lane turns
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kQH; ++i) {
+        const int h = qh0 + kQStep * i;
+        const __nv_bfloat16* qp = a.q + ((int64_t)b * a.Hq + g * a.r + h) * D + qt;
+        const uint32_t xq = h < a.r ? *reinterpret_cast<const uint32_t*>(qp) : 0u;
+        const uint32_t yq = h < a.r ? *reinterpret_cast<const uint32_t*>(qp + H2) : 0u;
+        const float x0 = bf16lo_to_f32(xq), x1 = bf16hi_to_f32(xq), y0 = bf16lo_to_f32(yq), y1 = bf16hi_to_f32(yq);
+        if (h < kR)
+          qbuf[h * (NJ * 8) + qj] =
+              make_float4(x0 * f.x - y0 * f.z, x1 * f.y - y1 * f.w, y0 * f.x + x0 * f.z, y1 * f.y + x1 * f.w);
+        qn += x0 * x0 + x1 * x1 + y0 * y0 + y1 * y1;  // (all heads together bound each)
+      }
+      __syncwarp();
+      uint64_t acc[4][kR], norm[4];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        uint64_t x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = bf16x2_f2(j == 0 ? xw[i].x : j == 1 ? xw[i].y : j == 2 ? xw[i].z : xw[i].w);
+          y[i] = bf16x2_f2(j == 0 ? yw[i].x : j == 1 ? yw[i].y : j == 2 ? yw[i].z : yw[i].w);
+          norm[i] = f2_fma(y[i], y[i], j == 0 ? f2_mul(x[i], x[i]) : f2_fma(x[i], x[i], norm[i]));
+          uint64_t c, sn;
+          lds2x64(ef[i] + j * 128, c, sn);
+          const uint64_t xr = f2_sub(f2_mul(x[i], c), f2_mul(y[i], sn));
+          y[i] = f2_fma(x[i], sn, f2_mul(y[i], c));
+          x[i] = xr;
+        }
+#pragma unroll
+        for (int h = 0; h < kR; ++h) {
+          uint64_t qa, qb;
+          lds2x64(qaddr + ((h ^ hx) * NJ + j) * 128, qa, qb);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[i][h] = f2_fma(y[i], qb, j == 0 ? f2_mul(x[i], qa) : f2_fma(x[i], qa, acc[i][h]));
+        }
+      }
+      float v[4][kR], big = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f2_unpack(norm[i], lo, hi);
+        big = max_nan(lo + hi, big);
+#pragma unroll
+        for (int h = 0; h < kR; ++h) {
+          f2_unpack(acc[i][h], lo, hi);
+          v[i][h] = lo + hi;
+        }
+      }
+      constexpr int kV = kR == 8 ? 4 : 2;
+      if constexpr (kR == 8) {
+#pragma unroll
+        for (int s = 4; s >= 1; s >>= 1)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < s; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h + s], s);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int h = 0; h < kR; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i + 2][h], 4);
+#pragma unroll
+          for (int s = 2; s >= 1; s >>= 1) {
+            if (kR > s) {
+#pragma unroll
+              for (int h = 0; h < s; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h + s], s);
+            } else {
+#pragma unroll
+              for (int h = 0; h < kR; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h], s);
+            }
+          }
+        }
+      }
+      // the best head; heads behind r take no part
+      const int kfirst = kR == 8 ? 4 * kg : 4 * kg + 2 * (pg >> 2);
+      float* out = a.scores + ((int64_t)b * a.Hkv + g) * a.max_pages + page0;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        float t = hx < a.r ? v[i][0] : -INFINITY;
+#pragma unroll
+        for (int s = 1; s < kR; s <<= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, s));
+        const int u = kfirst + i;
+        if (hx == 0 && (kR == 8 || (pg & 3) == 0) && page0 + u < sp.band)
+          out[u] = pages[16 * m + u] >= 0 ? t : -INFINITY;
+      }
+      // an upper bound of |q| |c| over the group: the sum over lanes of each lane's largest part
+#pragma unroll
+      for (int s = 1; s < 8; s <<= 1) big += __shfl_xor_sync(0xffffffffu, big, s);
+      big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 8));
+      big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 16));
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) qn += __shfl_xor_sync(0xffffffffu, qn, s);
+      if (lane == 0) a.bounds[((int64_t)b * a.Hkv + g) * a.bound_tiles + (page0 - sp.sink) / 16] =
+            (sqrtf(qn) + kTiny) * (sqrtf(big) + kTiny);
     }
-    // the best head; heads behind r take no part
-    const int kfirst = kR == 8 ? 4 * kg : 4 * kg + 2 * (pg >> 2);
-    float* out = a.scores + ((int64_t)b * a.Hkv + g) * a.max_pages + page0;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      float t = hx < a.r ? v[i][0] : -INFINITY;
-#pragma unroll
-      for (int s = 1; s < kR; s <<= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, s));
-      const int u = kfirst + i;
-      if (hx == 0 && (kR == 8 || (pg & 3) == 0) && page0 + u < sp.band)
-        out[u] = pages[16 * m + u] >= 0 ? t : -INFINITY;
-    }
-    // an upper bound of |q| |c| over the group: the sum over lanes of each lane's largest part
-#pragma unroll
-    for (int s = 1; s < 8; s <<= 1) big += __shfl_xor_sync(0xffffffffu, big, s);
-    big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 8));
-    big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 16));
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) qn += __shfl_xor_sync(0xffffffffu, qn, s);
-    if (lane == 0) a.bounds[((int64_t)b * a.Hkv + g) * a.bound_tiles + (page0 - sp.sink) / 16] =
-          (sqrtf(qn) + kTiny) * (sqrtf(big) + kTiny);
   }
 }
 
