@@ -15,6 +15,7 @@
 // to the lowest page.  Listed in ascending order, the rest of the row is -1.
 #include <algorithm>
 
+#include "jl_mma.cuh"
 #include "jl_paged.cuh"
 
 namespace jl {
@@ -22,6 +23,7 @@ namespace jl {
 namespace {
 
 constexpr int kSumThreads = 256;
+constexpr int kScoreThreads = 256;
 constexpr int kMaxTile = 128;       // pages per CTA of the score kernel, at most
 constexpr int kSelThreads = 512;
 constexpr int kRank = 128;          // pages between the edges that are ranked by comparing all
@@ -139,54 +141,52 @@ __device__ __forceinline__ PageSpan page_span(const PageSelectArgs& a, int b) {
 // Which page lies above a border must not depend on the order of a sum, so a score
 // is the fp64 value rounded to fp32.  Forming all of them in fp64 is bound by the
 // fp64 pipe and its conversions (110 us for eight sequences of 2048 pages, against
-// 5 us to read the summaries); instead every page gets an fp32 score with a bound
-// on its error, and only pages that the bound cannot place are scored in fp64.
+// 5 us to read the summaries); instead every page gets a score with a bound on its
+// error, and only pages that the bound cannot place are scored in fp64.
 //
-// fp32 score of 16 consecutive pages for one KV head, by one warp.  As in the
-// decode, the queries take R(dq - dk(c0)) for the group's first page and page u the
-// rest, dk(c_u) - dk(c0) = floor((rm + u P) / G) - u P with rm = c0 mod G, which
-// takes two values per u: a table of 32 rows per sequence.  A lane scores 4 pages
-// over D/16 pairs for every head, and eight lanes' sums meet in an exchange; slot i
-// of a lane is page 4 kg + (i ^ kx), slot h head h ^ hx, so that what an exchange
-// keeps is always the lower half of the slots.
+// Score of 16 consecutive pages for one KV head, by one warp: mma.sync m16n8k16 with
+// the query heads on the M axis and the pages on N, both sides turned in fp32 and
+// rounded to fp16 once (2^-11; a page's rounding errors decide only how many pages go
+// to fp64, about 36 of 65536).  As in the decode, the queries take R(dq - dk(c0)) for
+// the group's first page and page u the rest, dk(c_u) - dk(c0) = floor((rm + u P) / G)
+// - u P with rm = c0 mod G, which takes two values per u: a table of 32 rows per
+// sequence.  The k axis is dealt so that a lane's fragments are 16-byte pieces of a
+// summary: lane c4 of a page holds dims 8 (c4 + 4 j) + 0 .. 7 and those half a head on.
 //
-// Error of one score, in units of 2^-24 |q| |c|: the table's factors and the keys'
-// rotation 4, the queries' factors (the MUFU's 2^-21.2 each) and rotation 12, a chain
-// of eight fused sums, the sum of halves and three exchanges 12, the rounding to fp32
-// 1: below 30.  kScoreErr takes 64.
-constexpr float kScoreErr = 3.814697265625e-6f;    // 2^-18
-constexpr float kTiny = 8.470329472543003e-22f;    // 2^-70: lengths whose squares underflow
-
-__device__ __forceinline__ void lds2x64(uint32_t addr, uint64_t& a, uint64_t& b) {
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
-}
-__device__ __forceinline__ uint64_t bf16x2_f2(uint32_t w) { return f2_pack(bf16lo_to_f32(w), bf16hi_to_f32(w)); }
-
-// cos and sin of n theta, theta / 2 pi in 64-bit fixed point (whole turns fall off
-// the top): the phase is good to 2^-31 turns plus n 2^-56, the rest to fp32.
-__device__ __forceinline__ void sincos_fixed(int n, uint64_t turn, float* s, float* c) {
-  const uint32_t m = (uint32_t)(n < 0 ? -n : n);
-  const uint32_t ph = m * (uint32_t)(turn >> 32) + __umulhi(m, (uint32_t)turn);
-  float sn;
-  sincospif((float)(int32_t)ph * 4.656612873077393e-10f, &sn, c);  // 2 / 2^32
-  *s = n < 0 ? -sn : sn;
-}
+// Error of one score against |q| |c|: rounding both operands to fp16 2^-10, turning
+// them (the MUFU's 2^-21 and fp32 arithmetic) and summing 128 products in fp32 less
+// than 2^-16 together: below 1.02 2^-10, where kScoreErr takes 1.125 2^-10.  Below
+// fp16's normal range a value is off by up to 2^-25 instead, 2^-25 sqrt(128) of the
+// other side's length: kTiny adds that to the lengths.  Lengths that could leave
+// fp16's range give an infinite bound (every page of the row goes to fp64).
+constexpr float kScoreErr = 1.0986328125e-3f;  // 1.125 2^-10
+constexpr float kTiny = 3.5e-4f;               // 2^-25 sqrt(128) / kScoreErr, rounded up
+constexpr float kMaxLength = 60000.f;
 
 // The larger of two scores; a NaN stays.
 __device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }
 
-__host__ __device__ constexpr int score_threads(int kR) { return kR == 8 ? 128 : 256; }  // eight heads' sums: twice the registers
+// Two pairs turned by f = (c0, c1, s0, s1), rounded to fp16.
+__device__ __forceinline__ void turn_f16(uint64_t x, uint64_t y, const float4& f, uint32_t& xo, uint32_t& yo) {
+  const uint64_t c = f2_pack(f.x, f.y), sn = f2_pack(f.z, f.w);
+  const uint64_t xr = f2_sub(f2_mul(x, c), f2_mul(y, sn));
+  const uint64_t yr = f2_fma(x, sn, f2_mul(y, c));
+  float p, q;
+  f2_unpack(xr, p, q);
+  xo = pack_f16x2(p, q);
+  f2_unpack(yr, p, q);
+  yo = pack_f16x2(p, q);
+}
 
-// kR: query heads per KV head r, padded to 1, 2, 4 or 8.
-template <int D, int kR>
-__global__ void __launch_bounds__(score_threads(kR), 2)
-    page_score_kernel(const __grid_constant__ PageSelectArgs a) {
-  constexpr int H2 = D / 2, NP = D / 16, NJ = NP / 2;
-  constexpr int kQStep = D == 128 ? 1 : 2, kQH = D == 128 ? kR : (kR + 1) / 2;
-  constexpr int kThreads = score_threads(kR), kWarps = kThreads / 32;
-  __shared__ __align__(16) float4 etab[32 * NJ * 8];         // [u + 16 extra][j][lane] (c, c, s, s)
-  __shared__ __align__(16) float4 qbufs[kWarps][kR * NJ * 8];  // [head][j][lane] (x, x, y, y)
-  __shared__ int pages[kMaxTile];                            // the tile's pages in the pool, -1: none
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const __grid_constant__ PageSelectArgs a) {
+  constexpr int H2 = D / 2;
+  constexpr int NJ = D / 64;                   // 16-byte pieces of a lane in either half of a summary
+  constexpr int kWarps = kScoreThreads / 32;
+  constexpr int kERow = H2 / 2 + 4;            // float4s per row of the table (padded: two rows side by side)
+  __shared__ __align__(16) float4 etab[32 * kERow];      // [u + 16 extra][j][i][c4] (c, c, s, s)
+  __shared__ __align__(16) float4 csb_all[kWarps][H2 / 2];
+  __shared__ int pages[kMaxTile];              // the tile's pages in the pool, -1: none
   const int b = blockIdx.y;
   const PageSpan sp = page_span(a, b);
   const int p0 = sp.sink + blockIdx.x * a.tile_pages;
@@ -197,44 +197,33 @@ __global__ void __launch_bounds__(score_threads(kR), 2)
   const int G = (int)group_size(L, a.w_pretrained);
   const int dq = (int)(query_remote(L - 1, G, query_shift(a.w0, G, a.qshift)) - (L - 1));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kg = lane >> 3, pg = lane & 7;
-  const int qt = NP * pg + 2 * (D == 128 ? kg : (kg & 1));  // the pairs whose factors this lane forms
-  const int qj = (D == 128 ? kg : (kg & 1)) * 8 + pg;       // and their place in a buffer's row
-  const int qh0 = D == 128 ? 0 : kg >> 1;
+  const int c4 = lane & 3, hrow = lane >> 2;
+  // the two pairs whose factors this lane forms: place (j, i, c4) of a row is pairs 8 (c4 + 4 j) + 2 i, + 1
+  const int fl = lane % (H2 / 2);
+  const int ft = 8 * ((fl & 3) + 4 * (fl >> 4)) + 2 * ((fl >> 2) & 3);
   uint64_t turn0, turn1;
   {
     const uint64_t* tp = a.turn;  // a generic read: an indexed parameter read serialises
     asm volatile("" : "+l"(tp));
-    turn0 = tp[qt];
-    turn1 = tp[qt + 1];
+    turn0 = tp[ft];
+    turn1 = tp[ft + 1];
   }
-  auto factors = [&](int n) {
-    float4 f;
-    sincos_phase(n, turn0, &f.z, &f.x);
-    sincos_phase(n, turn1, &f.w, &f.y);
-    return f;
-  };
-  for (int i = threadIdx.x; i < 16 * groups; i += kThreads) {
+  for (int i = threadIdx.x; i < 16 * groups; i += kScoreThreads) {
     const int phys = p0 + i < sp.band ? a.block_table[(int64_t)b * a.max_pages + p0 + i] : -1;
     const bool ok = phys >= 0 && phys < a.num_pages;
     if (!ok && p0 + i < sp.band && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
     pages[i] = ok ? phys : -1;
   }
-  for (int row = kQStep * warp + qh0; row < 32; row += kQStep * kWarps) {
-    const int u = row & 15;
-    const int n = u * P / G + (row >> 4) - u * P;
+  for (int row = warp; row < 32; row += kWarps) {
+    const int u = row & 15, n = u * P / G + (row >> 4) - u * P;
     float4 f;
-    sincos_fixed(n, turn0, &f.z, &f.x);
-    sincos_fixed(n, turn1, &f.w, &f.y);
-    etab[row * (NJ * 8) + qj] = f;
+    sincos_phase(n, turn0, &f.z, &f.x);
+    sincos_phase(n, turn1, &f.w, &f.y);
+    etab[row * kERow + fl] = f;
   }
   __syncthreads();
-  const int hx = pg & (kR - 1), kx = kR == 8 ? 0 : 2 * (pg >> 2);
-  float4* qbuf = qbufs[warp];
-  const uint32_t qaddr = smem_addr(qbuf) + pg * 16, eaddr = smem_addr(etab) + pg * 16;
-  int rem[4];  // u P mod G of this lane's slots
-#pragma unroll
-  for (int i = 0; i < 4; ++i) rem[i] = (4 * kg + (i ^ kx)) * P % G;
+  float4* csb = csb_all[warp];
+  const int rem0 = hrow * P % G, rem1 = (hrow + 8) * P % G;  // u P mod G of this lane's two pages
   // A warp takes a group of 16 pages and a share of the KV heads: what depends on the
   // positions alone is formed once for them.
   const int shares = max(1, min(a.Hkv, kWarps / groups)), per = (a.Hkv + shares - 1) / shares;
@@ -243,129 +232,106 @@ __global__ void __launch_bounds__(score_threads(kR), 2)
     const int page0 = p0 + 16 * m;
     const int c0 = page0 * P + P / 2;
     const int q0 = c0 / G, rm = c0 - q0 * G;
-    const float4 f = factors(dq - (q0 - c0));
-    int phys[4];      // this lane's pages and their factor rows
-    uint32_t ef[4];
+    float4 f;
+    sincos_phase(dq - (q0 - c0), turn0, &f.z, &f.x);
+    sincos_phase(dq - (q0 - c0), turn1, &f.w, &f.y);
+    __syncwarp();
+    csb[fl] = f;
+    __syncwarp();
+    const int phys[2] = {pages[16 * m + hrow], pages[16 * m + 8 + hrow]};
+    const float4* er[2] = {etab + (hrow + (rm + rem0 >= G ? 16 : 0)) * kERow + c4,
+                           etab + (hrow + 8 + (rm + rem1 >= G ? 16 : 0)) * kERow + c4};
+    const int64_t row_len = (int64_t)a.Hkv * D;
+    const __nv_bfloat16* kp[2] = {a.summaries + max(phys[0], 0) * row_len + 8 * c4,
+                                  a.summaries + max(phys[1], 0) * row_len + 8 * c4};
+    uint4 k[2][2 * NJ];  // both pages' pieces: first halves, second halves
+    auto load = [&](int g) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int u = 4 * kg + (i ^ kx);
-      phys[i] = pages[16 * m + u];
-      ef[i] = eaddr + (u + (rm + rem[i] >= G ? 16 : 0)) * (NJ * 128);
-    }
-    for (int g = g0; g < g1; ++g) {
-      uint4 xw[4], yw[4];
+      for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        xw[i] = yw[i] = make_uint4(0, 0, 0, 0);
-        if (phys[i] >= 0) {
-          const __nv_bfloat16* k = a.summaries + ((int64_t)phys[i] * a.Hkv + g) * D + NP * pg;
-          if constexpr (D == 128) {
-            xw[i] = *reinterpret_cast<const uint4*>(k);
-            yw[i] = *reinterpret_cast<const uint4*>(k + H2);
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(k), y = *reinterpret_cast<const uint2*>(k + H2);
-            xw[i].x = x.x, xw[i].y = x.y, yw[i].x = y.x, yw[i].y = y.y;
-          }
+        for (int j = 0; j < NJ; ++j) {
+          k[nt][j] = *reinterpret_cast<const uint4*>(kp[nt] + g * D + 32 * j);
+          k[nt][NJ + j] = *reinterpret_cast<const uint4*>(kp[nt] + g * D + H2 + 32 * j);
         }
-      }
-      // the head's queries, turned for the group's first page
-      float qn = 0.f;  // |q|^2 of the heads this lane turns
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < kQH; ++i) {
-        const int h = qh0 + kQStep * i;
-        const __nv_bfloat16* qp = a.q + ((int64_t)b * a.Hq + g * a.r + h) * D + qt;
-        const uint32_t xq = h < a.r ? *reinterpret_cast<const uint32_t*>(qp) : 0u;
-        const uint32_t yq = h < a.r ? *reinterpret_cast<const uint32_t*>(qp + H2) : 0u;
-        const float x0 = bf16lo_to_f32(xq), x1 = bf16hi_to_f32(xq), y0 = bf16lo_to_f32(yq), y1 = bf16hi_to_f32(yq);
-        if (h < kR)
-          qbuf[h * (NJ * 8) + qj] =
-              make_float4(x0 * f.x - y0 * f.z, x1 * f.y - y1 * f.w, y0 * f.x + x0 * f.z, y1 * f.y + x1 * f.w);
-        qn += x0 * x0 + x1 * x1 + y0 * y0 + y1 * y1;  // (all heads together bound each)
-      }
-      __syncwarp();
-      uint64_t acc[4][kR], norm[4];
+    };
+    load(g0);
+#pragma unroll 1
+    for (int g = g0; g < g1; ++g) {
+      // the queries as A fragments (rows 8-15 stay zero), and |q|^2
+      uint32_t aq[NJ][4][2];
+      float qn = 0.f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        uint64_t x[4], y[4];
+        uint4 xw = make_uint4(0, 0, 0, 0), yw = xw;
+        if (hrow < a.r) {
+          const __nv_bfloat16* q = a.q + ((int64_t)b * a.Hq + g * a.r + hrow) * D + 8 * c4 + 32 * j;
+          xw = *reinterpret_cast<const uint4*>(q);
+          yw = *reinterpret_cast<const uint4*>(q + H2);
+        }
+        const uint32_t xs[4] = {xw.x, xw.y, xw.z, xw.w}, ys[4] = {yw.x, yw.y, yw.z, yw.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[i] = bf16x2_f2(j == 0 ? xw[i].x : j == 1 ? xw[i].y : j == 2 ? xw[i].z : xw[i].w);
-          y[i] = bf16x2_f2(j == 0 ? yw[i].x : j == 1 ? yw[i].y : j == 2 ? yw[i].z : yw[i].w);
-          norm[i] = f2_fma(y[i], y[i], j == 0 ? f2_mul(x[i], x[i]) : f2_fma(x[i], x[i], norm[i]));
-          uint64_t c, sn;
-          lds2x64(ef[i] + j * 128, c, sn);
-          const uint64_t xr = f2_sub(f2_mul(x[i], c), f2_mul(y[i], sn));
-          y[i] = f2_fma(x[i], sn, f2_mul(y[i], c));
-          x[i] = xr;
-        }
-#pragma unroll
-        for (int h = 0; h < kR; ++h) {
-          uint64_t qa, qb;
-          lds2x64(qaddr + ((h ^ hx) * NJ + j) * 128, qa, qb);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[i][h] = f2_fma(y[i], qb, j == 0 ? f2_mul(x[i], qa) : f2_fma(x[i], qa, acc[i][h]));
+          const uint64_t x = bf16x2_to_f2(xs[i]), y = bf16x2_to_f2(ys[i]);
+          float p0f, p1f;
+          f2_unpack(f2_fma(y, y, f2_mul(x, x)), p0f, p1f);
+          qn += p0f + p1f;
+          turn_f16(x, y, csb[(j * 4 + i) * 4 + c4], aq[j][i][0], aq[j][i][1]);
         }
       }
-      float v[4][kR], big = 0.f;
+      float acc[2][4], big = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float lo, hi;
-        f2_unpack(norm[i], lo, hi);
-        big = max_nan(lo + hi, big);
+      for (int nt = 0; nt < 2; ++nt) {
+        acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+        uint64_t norm = 0ull;
 #pragma unroll
-        for (int h = 0; h < kR; ++h) {
-          f2_unpack(acc[i][h], lo, hi);
-          v[i][h] = lo + hi;
-        }
-      }
-      constexpr int kV = kR == 8 ? 4 : 2;
-      if constexpr (kR == 8) {
+        for (int j = 0; j < NJ; ++j) {
+          const uint32_t xs[4] = {k[nt][j].x, k[nt][j].y, k[nt][j].z, k[nt][j].w};
+          const uint32_t ys[4] = {k[nt][NJ + j].x, k[nt][NJ + j].y, k[nt][NJ + j].z, k[nt][NJ + j].w};
+          uint32_t bx[4], by[4];
 #pragma unroll
-        for (int s = 4; s >= 1; s >>= 1)
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t x = bf16x2_to_f2(xs[i]), y = bf16x2_to_f2(ys[i]);
+            norm = f2_fma(y, y, f2_fma(x, x, norm));
+            turn_f16(x, y, er[nt][(j * 4 + i) * 4], bx[i], by[i]);
+          }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int h = 0; h < s; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h + s], s);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int h = 0; h < kR; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i + 2][h], 4);
-#pragma unroll
-          for (int s = 2; s >= 1; s >>= 1) {
-            if (kR > s) {
-#pragma unroll
-              for (int h = 0; h < s; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h + s], s);
-            } else {
-#pragma unroll
-              for (int h = 0; h < kR; ++h) v[i][h] += __shfl_xor_sync(0xffffffffu, v[i][h], s);
-            }
+          for (int i = 0; i < 4; i += 2) {
+            mma_f16(acc[nt], aq[j][i][0], 0u, aq[j][i + 1][0], 0u, bx[i], bx[i + 1]);
+            mma_f16(acc[nt], aq[j][i][1], 0u, aq[j][i + 1][1], 0u, by[i], by[i + 1]);
           }
         }
+        float lo, hi;
+        f2_unpack(norm, lo, hi);
+        lo += hi;  // this lane's part of its page's |c|^2
+        lo += __shfl_xor_sync(0xffffffffu, lo, 1);
+        lo += __shfl_xor_sync(0xffffffffu, lo, 2);
+        if (phys[nt] >= 0) big = max_nan(lo, big);
       }
-      // the best head; heads behind r take no part
-      const int kfirst = kR == 8 ? 4 * kg : 4 * kg + 2 * (pg >> 2);
+      if (g + 1 < g1) load(g + 1);
+      // the best head per page: lane (hrow, c4) holds head hrow of pages 8 nt + 2 c4 + {0, 1}
       float* out = a.scores + ((int64_t)b * a.Hkv + g) * a.max_pages + page0;
 #pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        float t = hx < a.r ? v[i][0] : -INFINITY;
+      for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int s = 1; s < kR; s <<= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, s));
-        const int u = kfirst + i;
-        if (hx == 0 && (kR == 8 || (pg & 3) == 0) && page0 + u < sp.band)
-          out[u] = pages[16 * m + u] >= 0 ? t : -INFINITY;
+        for (int e = 0; e < 2; ++e) {
+          float t = hrow < a.r ? acc[nt][e] : -INFINITY;
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, s));
+          const int u = 8 * nt + 2 * c4 + e;
+          if (hrow == 0 && page0 + u < sp.band) out[u] = pages[16 * m + u] >= 0 ? t : -INFINITY;
+        }
+      qn += __shfl_xor_sync(0xffffffffu, qn, 1);
+      qn += __shfl_xor_sync(0xffffffffu, qn, 2);
+#pragma unroll
+      for (int s = 4; s < 32; s <<= 1) {
+        qn = max_nan(qn, __shfl_xor_sync(0xffffffffu, qn, s));
+        big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, s));
       }
-      // an upper bound of |q| |c| over the group: the sum over lanes of each lane's largest part
-#pragma unroll
-      for (int s = 1; s < 8; s <<= 1) big += __shfl_xor_sync(0xffffffffu, big, s);
-      big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 8));
-      big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, 16));
-#pragma unroll
-      for (int s = 1; s < 32; s <<= 1) qn += __shfl_xor_sync(0xffffffffu, qn, s);
-      if (lane == 0) a.bounds[((int64_t)b * a.Hkv + g) * a.bound_tiles + (page0 - sp.sink) / 16] =
-            (sqrtf(qn) + kTiny) * (sqrtf(big) + kTiny);
+      if (lane == 0) {
+        const float ql = sqrtf(qn), cl = sqrtf(big);
+        a.bounds[((int64_t)b * a.Hkv + g) * a.bound_tiles + (page0 - sp.sink) / 16] =
+            ql < kMaxLength && cl < kMaxLength ? (ql + kTiny) * (cl + kTiny) : INFINITY;
+      }
     }
   }
 }
@@ -716,24 +682,6 @@ cudaError_t launch_page_summaries(const PageSummaryArgs& a, int D, cudaStream_t 
   return D == 128 ? launch_summary_d<128>(a, stream) : launch_summary_d<64>(a, stream);
 }
 
-namespace {
-
-template <int D>
-cudaError_t launch_score_d(const PageSelectArgs& a, cudaStream_t stream) {
-  const dim3 grid((unsigned)((a.max_pages + a.tile_pages - 1) / a.tile_pages), a.B);
-  if (a.r == 1)
-    page_score_kernel<D, 1><<<grid, score_threads(1), 0, stream>>>(a);
-  else if (a.r == 2)
-    page_score_kernel<D, 2><<<grid, score_threads(2), 0, stream>>>(a);
-  else if (a.r <= 4)
-    page_score_kernel<D, 4><<<grid, score_threads(4), 0, stream>>>(a);
-  else
-    page_score_kernel<D, 8><<<grid, score_threads(8), 0, stream>>>(a);
-  return cudaGetLastError();
-}
-
-}  // namespace
-
 cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream) {
   cudaError_t e;
   if (a.top_k > 0) {
@@ -744,8 +692,12 @@ cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream) {
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     a.tile_pages = kMaxTile;
     while (a.tile_pages > 16 && (a.max_pages + a.tile_pages - 1) / a.tile_pages * a.B < 2 * sms) a.tile_pages /= 2;
-    e = D == 128 ? launch_score_d<128>(a, stream) : launch_score_d<64>(a, stream);
-    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((a.max_pages + a.tile_pages - 1) / a.tile_pages), a.B);
+    if (D == 128)
+      page_score_kernel<128><<<grid, kScoreThreads, 0, stream>>>(a);
+    else
+      page_score_kernel<64><<<grid, kScoreThreads, 0, stream>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   // One CTA per 4096 pages, at most eight (the portable cluster size).
   int cl = 1;
