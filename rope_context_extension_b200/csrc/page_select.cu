@@ -25,6 +25,7 @@ namespace {
 constexpr int kSumThreads = 256;
 constexpr int kScoreThreads = 256;
 constexpr int kMaxTile = 128;       // pages per CTA of the score kernel, at most
+constexpr int kHeadBlock = 8;       // KV heads whose turned queries a CTA of the score kernel holds
 constexpr int kSelThreads = 512;
 constexpr int kRank = 128;          // pages between the edges that are ranked by comparing all
 
@@ -147,11 +148,10 @@ __device__ __forceinline__ PageSpan page_span(const PageSelectArgs& a, int b) {
 // Score of 16 consecutive pages for one KV head, by one warp: mma.sync m16n8k16 with
 // the query heads on the M axis and the pages on N, both sides turned in fp32 and
 // rounded to fp16 once (2^-11; a page's rounding errors decide only how many pages go
-// to fp64, about 36 of 65536).  As in the decode, the queries take R(dq - dk(c0)) for
-// the group's first page and page u the rest, dk(c_u) - dk(c0) = floor((rm + u P) / G)
-// - u P with rm = c0 mod G, which takes two values per u: a table of 32 rows per
-// sequence.  The k axis is dealt so that a lane's fragments are 16-byte pieces of a
-// summary: lane c4 of a page holds dims 8 (c4 + 4 j) + 0 .. 7 and those half a head on.
+// to fp64, about 36 of 65536).  The queries take R(dq) once per CTA, the pages R(dk(c))
+// from a table of the group's 16 positions that a warp forms for all its KV heads.  The
+// k axis is dealt so that a lane's fragments are 16-byte pieces of a summary: lane c4 of
+// a page holds dims 8 (c4 + 4 j) + 0 .. 7 and those half a head on.
 //
 // Error of one score against |q| |c|: rounding both operands to fp16 2^-10, turning
 // them (the MUFU's 2^-21 and fp32 arithmetic) and summing 128 products in fp32 less
@@ -164,7 +164,11 @@ constexpr float kTiny = 3.5e-4f;               // 2^-25 sqrt(128) / kScoreErr, r
 constexpr float kMaxLength = 60000.f;
 
 // The larger of two scores; a NaN stays.
-__device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 
 // Two pairs turned by f = (c0, c1, s0, s1), rounded to fp16.
 __device__ __forceinline__ void turn_f16(uint64_t x, uint64_t y, const float4& f, uint32_t& xo, uint32_t& yo) {
@@ -179,14 +183,23 @@ __device__ __forceinline__ void turn_f16(uint64_t x, uint64_t y, const float4& f
 }
 
 template <int D>
+struct ScoreSmem {
+  static constexpr int kRow = D / 4 + 4;  // float4s per row of a table (padded: two rows side by side)
+  float4 table[kScoreThreads / 32][16 * kRow];   // a warp's group: [u][j][i][c4] (c, c, s, s)
+  float4 qfactor[D / 4];                         // R(dq), a row of the same kind
+  uint4 q[kHeadBlock][D / 32][32];               // turned queries as A fragments
+  float qnorm[kHeadBlock];                       // |q| of the longest head
+  int pages[kMaxTile];                           // the tile's pages in the pool, -1: none
+};
+
+template <int D>
 __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const __grid_constant__ PageSelectArgs a) {
   constexpr int H2 = D / 2;
-  constexpr int NJ = D / 64;                   // 16-byte pieces of a lane in either half of a summary
+  constexpr int NJ = D / 64;  // 16-byte pieces of a lane in either half of a summary
   constexpr int kWarps = kScoreThreads / 32;
-  constexpr int kERow = H2 / 2 + 4;            // float4s per row of the table (padded: two rows side by side)
-  __shared__ __align__(16) float4 etab[32 * kERow];      // [u + 16 extra][j][i][c4] (c, c, s, s)
-  __shared__ __align__(16) float4 csb_all[kWarps][H2 / 2];
-  __shared__ int pages[kMaxTile];              // the tile's pages in the pool, -1: none
+  constexpr int kRow = ScoreSmem<D>::kRow;
+  extern __shared__ __align__(16) uint8_t score_smem[];
+  ScoreSmem<D>& sm = *reinterpret_cast<ScoreSmem<D>*>(score_smem);
   const int b = blockIdx.y;
   const PageSpan sp = page_span(a, b);
   const int p0 = sp.sink + blockIdx.x * a.tile_pages;
@@ -208,129 +221,144 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const __gr
     turn0 = tp[ft];
     turn1 = tp[ft + 1];
   }
+  auto factors = [&](int n) {
+    float4 f;
+    sincos_phase(n, turn0, &f.z, &f.x);
+    sincos_phase(n, turn1, &f.w, &f.y);
+    return f;
+  };
   for (int i = threadIdx.x; i < 16 * groups; i += kScoreThreads) {
     const int phys = p0 + i < sp.band ? a.block_table[(int64_t)b * a.max_pages + p0 + i] : -1;
     const bool ok = phys >= 0 && phys < a.num_pages;
     if (!ok && p0 + i < sp.band && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
-    pages[i] = ok ? phys : -1;
+    sm.pages[i] = ok ? phys : -1;
   }
-  for (int row = warp; row < 32; row += kWarps) {
-    const int u = row & 15, n = u * P / G + (row >> 4) - u * P;
-    float4 f;
-    sincos_phase(n, turn0, &f.z, &f.x);
-    sincos_phase(n, turn1, &f.w, &f.y);
-    etab[row * kERow + fl] = f;
-  }
-  __syncthreads();
-  float4* csb = csb_all[warp];
-  const int rem0 = hrow * P % G, rem1 = (hrow + 8) * P % G;  // u P mod G of this lane's two pages
-  // A warp takes a group of 16 pages and a share of the KV heads: what depends on the
-  // positions alone is formed once for them.
-  const int shares = max(1, min(a.Hkv, kWarps / groups)), per = (a.Hkv + shares - 1) / shares;
-  for (int w = warp; w < groups * shares; w += kWarps) {
-    const int m = w / shares, g0 = (w - m * shares) * per, g1 = min(a.Hkv, g0 + per);
-    const int page0 = p0 + 16 * m;
-    const int c0 = page0 * P + P / 2;
-    const int q0 = c0 / G, rm = c0 - q0 * G;
-    float4 f;
-    sincos_phase(dq - (q0 - c0), turn0, &f.z, &f.x);
-    sincos_phase(dq - (q0 - c0), turn1, &f.w, &f.y);
-    __syncwarp();
-    csb[fl] = f;
-    __syncwarp();
-    const int phys[2] = {pages[16 * m + hrow], pages[16 * m + 8 + hrow]};
-    const float4* er[2] = {etab + (hrow + (rm + rem0 >= G ? 16 : 0)) * kERow + c4,
-                           etab + (hrow + 8 + (rm + rem1 >= G ? 16 : 0)) * kERow + c4};
-    const int64_t row_len = (int64_t)a.Hkv * D;
-    const __nv_bfloat16* kp[2] = {a.summaries + max(phys[0], 0) * row_len + 8 * c4,
-                                  a.summaries + max(phys[1], 0) * row_len + 8 * c4};
-    uint4 k[2][2 * NJ];  // both pages' pieces: first halves, second halves
-    auto load = [&](int g) {
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          k[nt][j] = *reinterpret_cast<const uint4*>(kp[nt] + g * D + 32 * j);
-          k[nt][NJ + j] = *reinterpret_cast<const uint4*>(kp[nt] + g * D + H2 + 32 * j);
-        }
-    };
-    load(g0);
-#pragma unroll 1
-    for (int g = g0; g < g1; ++g) {
-      // the queries as A fragments (rows 8-15 stay zero), and |q|^2
-      uint32_t aq[NJ][4][2];
+  if (warp == 0) sm.qfactor[fl] = factors(dq);
+  float4* table = sm.table[warp];
+  for (int gb = 0; gb < a.Hkv; gb += kHeadBlock) {
+    const int heads = min(kHeadBlock, a.Hkv - gb);
+    __syncthreads();
+    // the queries as A fragments (rows 8-15 stay zero), and |q|
+    for (int g = warp; g < heads; g += kWarps) {
       float qn = 0.f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         uint4 xw = make_uint4(0, 0, 0, 0), yw = xw;
         if (hrow < a.r) {
-          const __nv_bfloat16* q = a.q + ((int64_t)b * a.Hq + g * a.r + hrow) * D + 8 * c4 + 32 * j;
+          const __nv_bfloat16* q = a.q + ((int64_t)b * a.Hq + (gb + g) * a.r + hrow) * D + 8 * c4 + 32 * j;
           xw = *reinterpret_cast<const uint4*>(q);
           yw = *reinterpret_cast<const uint4*>(q + H2);
         }
         const uint32_t xs[4] = {xw.x, xw.y, xw.z, xw.w}, ys[4] = {yw.x, yw.y, yw.z, yw.w};
+        uint32_t xo[4], yo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint64_t x = bf16x2_to_f2(xs[i]), y = bf16x2_to_f2(ys[i]);
-          float p0f, p1f;
-          f2_unpack(f2_fma(y, y, f2_mul(x, x)), p0f, p1f);
-          qn += p0f + p1f;
-          turn_f16(x, y, csb[(j * 4 + i) * 4 + c4], aq[j][i][0], aq[j][i][1]);
+          float n0, n1;
+          f2_unpack(f2_fma(y, y, f2_mul(x, x)), n0, n1);
+          qn += n0 + n1;
+          turn_f16(x, y, sm.qfactor[(j * 4 + i) * 4 + c4], xo[i], yo[i]);
         }
+        sm.q[g][2 * j][lane] = make_uint4(xo[0], xo[1], xo[2], xo[3]);
+        sm.q[g][2 * j + 1][lane] = make_uint4(yo[0], yo[1], yo[2], yo[3]);
       }
-      float acc[2][4], big = 0.f;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-        uint64_t norm = 0ull;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const uint32_t xs[4] = {k[nt][j].x, k[nt][j].y, k[nt][j].z, k[nt][j].w};
-          const uint32_t ys[4] = {k[nt][NJ + j].x, k[nt][NJ + j].y, k[nt][NJ + j].z, k[nt][NJ + j].w};
-          uint32_t bx[4], by[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint64_t x = bf16x2_to_f2(xs[i]), y = bf16x2_to_f2(ys[i]);
-            norm = f2_fma(y, y, f2_fma(x, x, norm));
-            turn_f16(x, y, er[nt][(j * 4 + i) * 4], bx[i], by[i]);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            mma_f16(acc[nt], aq[j][i][0], 0u, aq[j][i + 1][0], 0u, bx[i], bx[i + 1]);
-            mma_f16(acc[nt], aq[j][i][1], 0u, aq[j][i + 1][1], 0u, by[i], by[i + 1]);
-          }
-        }
-        float lo, hi;
-        f2_unpack(norm, lo, hi);
-        lo += hi;  // this lane's part of its page's |c|^2
-        lo += __shfl_xor_sync(0xffffffffu, lo, 1);
-        lo += __shfl_xor_sync(0xffffffffu, lo, 2);
-        if (phys[nt] >= 0) big = max_nan(lo, big);
-      }
-      if (g + 1 < g1) load(g + 1);
-      // the best head per page: lane (hrow, c4) holds head hrow of pages 8 nt + 2 c4 + {0, 1}
-      float* out = a.scores + ((int64_t)b * a.Hkv + g) * a.max_pages + page0;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float t = hrow < a.r ? acc[nt][e] : -INFINITY;
-#pragma unroll
-          for (int s = 4; s < 32; s <<= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, s));
-          const int u = 8 * nt + 2 * c4 + e;
-          if (hrow == 0 && page0 + u < sp.band) out[u] = pages[16 * m + u] >= 0 ? t : -INFINITY;
-        }
       qn += __shfl_xor_sync(0xffffffffu, qn, 1);
       qn += __shfl_xor_sync(0xffffffffu, qn, 2);
 #pragma unroll
-      for (int s = 4; s < 32; s <<= 1) {
-        qn = max_nan(qn, __shfl_xor_sync(0xffffffffu, qn, s));
-        big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, s));
+      for (int s = 4; s < 32; s <<= 1) qn = max_nan(qn, __shfl_xor_sync(0xffffffffu, qn, s));
+      if (lane == 0) sm.qnorm[g] = sqrtf(qn);
+    }
+    __syncthreads();
+    // A warp takes a group of 16 pages and a share of the heads.
+    const int shares = max(1, min(heads, kWarps / groups)), per = (heads + shares - 1) / shares;
+    for (int w = warp; w < groups * shares; w += kWarps) {
+      const int m = w / shares, g0 = (w - m * shares) * per, g1 = min(heads, g0 + per);
+      if (g0 >= g1) continue;
+      const int page0 = p0 + 16 * m;
+      const int phys[2] = {sm.pages[16 * m + hrow], sm.pages[16 * m + 8 + hrow]};
+      const int64_t row_len = (int64_t)a.Hkv * D;
+      const __nv_bfloat16* kp[2] = {a.summaries + max(phys[0], 0) * row_len + gb * D + 8 * c4,
+                                    a.summaries + max(phys[1], 0) * row_len + gb * D + 8 * c4};
+      uint4 k[2][2 * NJ];  // both pages' pieces: first halves, second halves
+      auto load = [&](int g) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            k[nt][j] = *reinterpret_cast<const uint4*>(kp[nt] + g * D + 32 * j);
+            k[nt][NJ + j] = *reinterpret_cast<const uint4*>(kp[nt] + g * D + H2 + 32 * j);
+          }
+      };
+      load(g0);
+      __syncwarp();
+      {
+        int c = page0 * P + P / 2;
+#pragma unroll 4
+        for (int u = 0; u < 16; ++u, c += P) table[u * kRow + fl] = factors(c / G - c);
       }
-      if (lane == 0) {
-        const float ql = sqrtf(qn), cl = sqrtf(big);
-        a.bounds[((int64_t)b * a.Hkv + g) * a.bound_tiles + (page0 - sp.sink) / 16] =
-            ql < kMaxLength && cl < kMaxLength ? (ql + kTiny) * (cl + kTiny) : INFINITY;
+      __syncwarp();
+      const float4* er[2] = {table + hrow * kRow + c4, table + (hrow + 8) * kRow + c4};
+#pragma unroll 1
+      for (int g = g0; g < g1; ++g) {
+        uint4 aq[2 * NJ];
+#pragma unroll
+        for (int j = 0; j < 2 * NJ; ++j) aq[j] = sm.q[g][j][lane];
+        float acc[2][4], big = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+          uint64_t norm = 0ull;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const uint32_t xs[4] = {k[nt][j].x, k[nt][j].y, k[nt][j].z, k[nt][j].w};
+            const uint32_t ys[4] = {k[nt][NJ + j].x, k[nt][NJ + j].y, k[nt][NJ + j].z, k[nt][NJ + j].w};
+            uint32_t bx[4], by[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint64_t x = bf16x2_to_f2(xs[i]), y = bf16x2_to_f2(ys[i]);
+              norm = f2_fma(y, y, f2_fma(x, x, norm));
+              turn_f16(x, y, er[nt][(j * 4 + i) * 4], bx[i], by[i]);
+            }
+            mma_f16(acc[nt], aq[2 * j].x, 0u, aq[2 * j].y, 0u, bx[0], bx[1]);
+            mma_f16(acc[nt], aq[2 * j].z, 0u, aq[2 * j].w, 0u, bx[2], bx[3]);
+            mma_f16(acc[nt], aq[2 * j + 1].x, 0u, aq[2 * j + 1].y, 0u, by[0], by[1]);
+            mma_f16(acc[nt], aq[2 * j + 1].z, 0u, aq[2 * j + 1].w, 0u, by[2], by[3]);
+          }
+          float lo, hi;
+          f2_unpack(norm, lo, hi);
+          lo += hi;  // this lane's part of its page's |c|^2
+          lo += __shfl_xor_sync(0xffffffffu, lo, 1);
+          lo += __shfl_xor_sync(0xffffffffu, lo, 2);
+          big = max_nan(lo, big);  // (page 0's in the place of a page that is not there)
+        }
+        if (g + 1 < g1) load(g + 1);
+        // the best head per page: lane (hrow, c4) holds head hrow of pages 8 nt + 2 c4 + {0, 1}
+        float* out = a.scores + ((int64_t)b * a.Hkv + gb + g) * a.max_pages + page0;
+        float t[2][2];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            t[nt][e] = hrow < a.r ? acc[nt][e] : -INFINITY;
+            for (int s = 4; s < 4 * a.r; s <<= 1)
+              t[nt][e] = max_nan(t[nt][e], __shfl_xor_sync(0xffffffffu, t[nt][e], s));
+          }
+        if (hrow == 0) {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int u = 8 * nt + 2 * c4 + e;
+              if (page0 + u < sp.band) out[u] = sm.pages[16 * m + u] >= 0 ? t[nt][e] : -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) big = max_nan(big, __shfl_xor_sync(0xffffffffu, big, s));
+        if (lane == 0) {
+          const float ql = sm.qnorm[g], cl = sqrtf(big);
+          a.bounds[((int64_t)b * a.Hkv + gb + g) * a.bound_tiles + (page0 - sp.sink) / 16] =
+              ql < kMaxLength && cl < kMaxLength ? (ql + kTiny) * (cl + kTiny) : INFINITY;
+        }
       }
     }
   }
@@ -682,6 +710,20 @@ cudaError_t launch_page_summaries(const PageSummaryArgs& a, int D, cudaStream_t 
   return D == 128 ? launch_summary_d<128>(a, stream) : launch_summary_d<64>(a, stream);
 }
 
+namespace {
+
+template <int D>
+cudaError_t launch_score(const PageSelectArgs& a, dim3 grid, cudaStream_t stream) {
+  auto k = page_score_kernel<D>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(ScoreSmem<D>));
+  if (e != cudaSuccess) return e;
+  k<<<grid, kScoreThreads, sizeof(ScoreSmem<D>), stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream) {
   cudaError_t e;
   if (a.top_k > 0) {
@@ -693,11 +735,7 @@ cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream) {
     a.tile_pages = kMaxTile;
     while (a.tile_pages > 16 && (a.max_pages + a.tile_pages - 1) / a.tile_pages * a.B < 2 * sms) a.tile_pages /= 2;
     const dim3 grid((unsigned)((a.max_pages + a.tile_pages - 1) / a.tile_pages), a.B);
-    if (D == 128)
-      page_score_kernel<128><<<grid, kScoreThreads, 0, stream>>>(a);
-    else
-      page_score_kernel<64><<<grid, kScoreThreads, 0, stream>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = D == 128 ? launch_score<128>(a, grid, stream) : launch_score<64>(a, grid, stream)) != cudaSuccess) return e;
   }
   // One CTA per 4096 pages, at most eight (the portable cluster size).
   int cl = 1;
