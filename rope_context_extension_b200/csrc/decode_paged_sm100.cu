@@ -841,11 +841,8 @@ cudaError_t launch_dp(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Pa
 }  // namespace
 
 int decode_paged_max_ctas() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 148;
-  return n < PgCfg<128>::kMaxParts ? n : PgCfg<128>::kMaxParts;
+  const int n = current_device_sms();
+  return n == 0 ? 148 : n < PgCfg<128>::kMaxParts ? n : PgCfg<128>::kMaxParts;
 }
 int decode_paged_warps() { return kWarps; }
 

@@ -2,6 +2,8 @@
 // the public surface is jl_api.h).
 #pragma once
 
+#include <atomic>
+
 #include "jl_kernels.cuh"
 
 namespace jl {
@@ -132,6 +134,17 @@ __device__ __forceinline__ void sincos_phase(int n, uint64_t turn, float* s, flo
   const float sn = __sinf(x);
   *s = n < 0 ? -sn : sn;
   *c = __cosf(x);
+}
+
+// SMs of the current device (looked up once per device), or 0 when there is none.
+inline int current_device_sms() {
+  static std::atomic<int> cached[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64 && (n = cached[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 0;
+  if (dev >= 0 && dev < 64) cached[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 // A sequence's length as the paged operators take it: 0 .. max_pages * page_size,

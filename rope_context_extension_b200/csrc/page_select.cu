@@ -23,6 +23,7 @@ namespace jl {
 namespace {
 
 constexpr int kSumThreads = 256;
+constexpr int kSumBlocksPerSm = 3;  // resident at 80 registers a thread
 constexpr int kScoreThreads = 256;
 constexpr int kMaxTile = 128;       // pages per CTA of the score kernel, at most
 constexpr int kHeadBlock = 8;       // KV heads whose turned queries a CTA of the score kernel holds
@@ -43,7 +44,7 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
 // Horner's rule in R(-step): sum_i R(-step i) k_{step i + grp}, so that two fixed
 // rotations per lane, formed once per warp, serve every page.
 template <int D>
-__global__ void __launch_bounds__(kSumThreads) page_summary_kernel(const __grid_constant__ PageSummaryArgs a) {
+__global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm) page_summary_kernel(const __grid_constant__ PageSummaryArgs a) {
   constexpr int H2 = D / 2;
   constexpr int kLanes = D / 16;
   constexpr int kStep = 32 / kLanes;  // rows per pass
@@ -691,15 +692,10 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
 
 template <int D>
 cudaError_t launch_summary_d(const PageSummaryArgs& a, cudaStream_t stream) {
-  int dev = 0, sms = 148, per_sm = 0;
-  cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, page_summary_kernel<D>, kSumThreads, 0)) !=
-      cudaSuccess)
-    return e;
+  const int sms = current_device_sms();
+  if (sms == 0) return cudaErrorNoDevice;
   const int64_t tasks = (int64_t)a.B * a.pages_per_seq * a.Hkv;
-  const int64_t blocks = std::min<int64_t>((tasks + kSumThreads / 32 - 1) / (kSumThreads / 32), (int64_t)sms * per_sm);
+  const int64_t blocks = std::min<int64_t>((tasks + kSumThreads / 32 - 1) / (kSumThreads / 32), (int64_t)sms * kSumBlocksPerSm);
   page_summary_kernel<D><<<(unsigned)blocks, kSumThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
@@ -729,9 +725,8 @@ cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream) {
   if (a.top_k > 0) {
     // Tiles of up to 128 pages share a factor table; smaller ones while the tiles do
     // not fill the GPU (two CTAs per SM).
-    int dev = 0, sms = 148;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const int sms = current_device_sms();
+    if (sms == 0) return cudaErrorNoDevice;
     a.tile_pages = kMaxTile;
     while (a.tile_pages > 16 && (a.max_pages + a.tile_pages - 1) / a.tile_pages * a.B < 2 * sms) a.tile_pages /= 2;
     const dim3 grid((unsigned)((a.max_pages + a.tile_pages - 1) / a.tile_pages), a.B);

@@ -25,6 +25,7 @@ namespace jl {
 namespace {
 
 constexpr int kNrThreads = 256;
+constexpr int kBlocksPerSm = 3;  // resident at 80 registers a thread
 
 __device__ __forceinline__ void bf16x8_to_f32(const uint4& w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -41,7 +42,7 @@ __device__ __forceinline__ uint4 f32_to_bf16x8(const float (&x)[8]) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+__global__ void __launch_bounds__(kNrThreads, kBlocksPerSm) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int H2 = D / 2;
   constexpr int kLanes = D / 16;       // lanes per head row
   constexpr int kRows = 32 / kLanes;   // head rows per pass of a warp
@@ -154,24 +155,20 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_cons
 template <int D>
 cudaError_t launch_d(NormRopeArgs& a, cudaStream_t stream) {
   constexpr int kRows = 512 / D;
-  int dev = 0, sms = 148, per_sm = 0;
-  cudaError_t e;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_rope_kernel<D>, kNrThreads, 0)) != cudaSuccess)
-    return e;
+  const int sms = current_device_sms();
+  if (sms == 0) return cudaErrorNoDevice;
   const int heads = a.Hq + a.Hkv + (a.v != nullptr ? a.Hkv : 0);
   const int passes = (heads + kRows - 1) / kRows;
   // One pass of a warp per task while the tokens do not fill the GPU's warps (a
   // decode step's latency); whole tokens per task (the factors formed once) when
   // they do.
-  const int64_t warps = (int64_t)sms * per_sm * (kNrThreads / 32);
+  const int64_t warps = (int64_t)sms * kBlocksPerSm * (kNrThreads / 32);
   int64_t per_task = ((int64_t)a.T * passes + warps - 1) / warps;
   if (per_task > passes) per_task = passes;
   a.heads_per_task = per_task * kRows;
   a.tasks_per_token = (int)((passes + per_task - 1) / per_task);
   const int64_t tasks = (int64_t)a.T * a.tasks_per_token;
-  const int64_t blocks = std::min<int64_t>((tasks + kNrThreads / 32 - 1) / (kNrThreads / 32), (int64_t)sms * per_sm);
+  const int64_t blocks = std::min<int64_t>((tasks + kNrThreads / 32 - 1) / (kNrThreads / 32), (int64_t)sms * kBlocksPerSm);
   norm_rope_kernel<D><<<(unsigned)blocks, kNrThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }

@@ -46,6 +46,7 @@ EXPORTED_SYMBOLS = (
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libjetlong.so")
 _lib = None
+_torch_module = None
 
 
 class _PagedKV(ctypes.Structure):
@@ -142,6 +143,15 @@ def lib() -> ctypes.CDLL:
     L.jl_wait_timeout_check.restype = c_i
     _lib = L
     return L
+
+
+def _torch():
+    """torch, imported with the first call that needs it."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _check(status: int, where: str):
@@ -451,11 +461,16 @@ def jl_wait_timeout_check(dev_error, timeout_s: float = 0.2, stream=None):
 # tensor of a call lives on the same device, which need not be the current one.
 # ---------------------------------------------------------------------------
 def _check_on(dev, specs):
-    """specs: (tensor, name, dtype, shape or None) of contiguous tensors on device dev."""
+    """specs: (tensor, name, dtype, shape) of contiguous tensors on device dev.  (One pass of
+    cheap tests: a decode step's calls are as long as their host side.)"""
     for t, name, dtype, shape in specs:
-        _check_tensor(t, name, dtype, shape)
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{dev}")
+        try:
+            ok = t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+        except AttributeError:
+            ok = False
+        if not ok:
+            _check_tensor(t, name, dtype, shape)
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
 def _check_opt(dev, t, name, dtype, shape):
@@ -463,14 +478,28 @@ def _check_opt(dev, t, name, dtype, shape):
         _check_on(dev, ((t, name, dtype, shape),))
 
 
+def _device_of(t, name):
+    try:
+        dev = t.get_device()
+    except AttributeError:
+        dev = -1
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _check_error_word(dev, t):
+    if t is not None:
+        _check_on(dev, ((t, "dev_error", _torch().int32, t.shape),))
+
+
 def _head_rows(t, name, T, H, D, dev):
     """Token stride of a [T, H, D] bf16 view whose heads are contiguous."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != (T, H, D):
+    if _device_of(t, name) != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.dtype is not _torch().bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.shape != (T, H, D):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H, D)}")
     st = t.stride()
     if st[2] != 1 or (H > 1 and st[1] != D):
@@ -479,14 +508,14 @@ def _head_rows(t, name, T, H, D, dev):
 
 
 def _paged_kv(k_pages, v_pages, dev, heads=None, head_dim=None):
-    import torch
+    bf16 = _torch().bfloat16
     for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
         if t is None and name == "v_pages":
             continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
-        if t.dtype != torch.bfloat16:
-            raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if _device_of(t, name) != dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+        if t.dtype is not bf16:
+            raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
         if t.dim() != 4 or t.stride(3) != 1:
             raise ValueError(f"{name} must be [num_pages, page_size, Hkv, D] with contiguous rows")
     n, P, H, D = k_pages.shape
@@ -503,17 +532,32 @@ def _paged_kv(k_pages, v_pages, dev, heads=None, head_dim=None):
     return _PagedKV(k_pages.data_ptr(), 0 if v_pages is None else v_pages.data_ptr(), n, sp, sr, sh, P)
 
 
-def _on_device(dev):
-    """A context with device dev current (none needed when it is already)."""
-    import contextlib
-    import torch
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+def _call(dev, fn, where, *args, stream=None):
+    """fn(*args, stream) with device dev current and the caller's stream, or the current one of dev.
+    (The two private getters are what torch's own generated launchers call: 0.1 us each, against
+    1.5 us for a Stream object.)"""
+    c = _torch()._C
+    if c._cuda_getDevice() == dev:
+        if stream is None:
+            stream = c._cuda_getCurrentRawStream(dev)
+        st = fn(*args, getattr(stream, "cuda_stream", stream))
+    else:
+        with _torch().cuda.device(dev):
+            if stream is None:
+                stream = c._cuda_getCurrentRawStream(dev)
+            st = fn(*args, getattr(stream, "cuda_stream", stream))
+    if st != 0:
+        raise JetLongError(st, where)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _workspace(dev, workspace):
     if workspace is None:
         return 0
-    if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+    if _device_of(workspace, "workspace") != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
     return workspace.numel() * workspace.element_size()
 
@@ -524,22 +568,20 @@ def jl_qk_norm_rope(q, k, q_weight, k_weight, positions, q_out, k_out, *, eps: f
     k [T, Hkv, D] (bf16, CUDA; views of a fused projection are fine), weights [D] bf16 or None
     (no norm on that side), positions int32 [T] (-1: padded token, left alone), q_out / k_out
     contiguous (they may be q / k)."""
-    import torch
+    torch = _torch()
     T, Hq, D = q.shape
     Hkv = k.shape[1]
-    dev = q.get_device()
+    dev = _device_of(q, "q")
     qs, ks = _head_rows(q, "q", T, Hq, D, dev), _head_rows(k, "k", T, Hkv, D, dev)
     bf16, i32 = torch.bfloat16, torch.int32
     _check_on(dev, ((positions, "positions", i32, (T,)), (q_out, "q_out", bf16, (T, Hq, D)),
                     (k_out, "k_out", bf16, (T, Hkv, D))))
     _check_opt(dev, q_weight, "q_weight", bf16, (D,))
     _check_opt(dev, k_weight, "k_weight", bf16, (D,))
-    _check_opt(dev, dev_error, "dev_error", i32, None)
-    with _on_device(dev):
-        st = lib().jl_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), float(eps),
-                                   _ptr(positions), _ptr(q_out), _ptr(k_out), T, Hq, Hkv, D, float(rope_base),
-                                   _ptr(dev_error), _stream(stream))
-    _check(st, "jl_qk_norm_rope")
+    _check_error_word(dev, dev_error)
+    _call(dev, lib().jl_qk_norm_rope, "jl_qk_norm_rope", q.data_ptr(), qs, k.data_ptr(), ks, _addr(q_weight), _addr(k_weight),
+          float(eps), positions.data_ptr(), q_out.data_ptr(), _addr(k_out), T, Hq, Hkv, D, float(rope_base), _addr(dev_error),
+          stream=stream)
 
 
 def jl_qk_norm_rope_append_paged(q, k, v, q_weight, k_weight, seq_ids, positions, block_table, q_out, k_pages,
@@ -547,10 +589,10 @@ def jl_qk_norm_rope_append_paged(q, k, v, q_weight, k_weight, seq_ids, positions
     """jl_qk_norm_rope whose keys, and the values v [T, Hkv, D], go to row positions[t] of
     sequence seq_ids[t] (int32 [T], a row of block_table int32 [B, max_pages]) of the paged
     cache; k_out [T, Hkv, D] (or None) receives the keys too."""
-    import torch
+    torch = _torch()
     T, Hq, D = q.shape
     Hkv = k.shape[1]
-    dev = q.get_device()
+    dev = _device_of(q, "q")
     qs, ks = _head_rows(q, "q", T, Hq, D, dev), _head_rows(k, "k", T, Hkv, D, dev)
     vs = _head_rows(v, "v", T, Hkv, D, dev)
     bf16, i32 = torch.bfloat16, torch.int32
@@ -560,14 +602,12 @@ def jl_qk_norm_rope_append_paged(q, k, v, q_weight, k_weight, seq_ids, positions
     _check_opt(dev, k_out, "k_out", bf16, (T, Hkv, D))
     _check_opt(dev, q_weight, "q_weight", bf16, (D,))
     _check_opt(dev, k_weight, "k_weight", bf16, (D,))
-    _check_opt(dev, dev_error, "dev_error", i32, None)
+    _check_error_word(dev, dev_error)
     kv = _paged_kv(k_pages, v_pages, dev, Hkv, D)
-    with _on_device(dev):
-        st = lib().jl_qk_norm_rope_append_paged(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight),
-                                                _ptr(k_weight), float(eps), _ptr(seq_ids), _ptr(positions),
-                                                _ptr(q_out), _ptr(k_out), ctypes.byref(kv), _ptr(block_table), M, T,
-                                                B, Hq, Hkv, D, float(rope_base), _ptr(dev_error), _stream(stream))
-    _check(st, "jl_qk_norm_rope_append_paged")
+    _call(dev, lib().jl_qk_norm_rope_append_paged, "jl_qk_norm_rope_append_paged", q.data_ptr(), qs, k.data_ptr(), ks,
+          v.data_ptr(), vs, _addr(q_weight), _addr(k_weight), float(eps), seq_ids.data_ptr(), positions.data_ptr(), q_out.data_ptr(),
+          _addr(k_out), ctypes.byref(kv), block_table.data_ptr(), M, T, B, Hq, Hkv, D, float(rope_base), _addr(dev_error),
+          stream=stream)
 
 
 def jl_decode_paged_workspace_bytes(Hq: int, Hkv: int, head_dim: int) -> int:
@@ -575,15 +615,15 @@ def jl_decode_paged_workspace_bytes(Hq: int, Hkv: int, head_dim: int) -> int:
 
 
 def _decode_paged_tensors(q, k_pages, v_pages, block_table, seq_lens, o, lse, workspace, dev_error):
-    import torch
+    torch = _torch()
     B, Hq, D = q.shape
-    dev = q.get_device()
+    dev = _device_of(q, "q")
     bf16, i32 = torch.bfloat16, torch.int32
     M = block_table.shape[1]
-    _check_on(dev, ((q, "q", bf16, None), (block_table, "block_table", i32, (B, M)),
+    _check_on(dev, ((q, "q", bf16, (B, Hq, D)), (block_table, "block_table", i32, (B, M)),
                     (seq_lens, "seq_lens", i32, (B,)), (o, "o", bf16, (B, Hq, D))))
     _check_opt(dev, lse, "lse", torch.float32, (B, Hq))
-    _check_opt(dev, dev_error, "dev_error", i32, None)
+    _check_error_word(dev, dev_error)
     kv = _paged_kv(k_pages, v_pages, dev)
     if k_pages.shape[3] != D:
         raise ValueError(f"k_pages holds rows of {k_pages.shape[3]}, expected {D}")
@@ -598,12 +638,10 @@ def jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seq_lens, o, lse, 
     zero-initialised uint8 CUDA tensor of jl_decode_paged_workspace_bytes(...) bytes."""
     B, Hq, Hkv, D, M, dev, kv, ws_bytes = _decode_paged_tensors(q, k_pages, v_pages, block_table, seq_lens, o, lse,
                                                                 workspace, dev_error)
-    with _on_device(dev):
-        st = lib().jl_bifocal_decode_paged(_ptr(q), ctypes.byref(kv), _ptr(block_table), M, _ptr(seq_lens), _ptr(o),
-                                           _ptr(lse), B, Hq, Hkv, D, int(w0), int(w_pretrained), float(rope_base),
-                                           float(softmax_scale), int(mode), _ptr(workspace), ws_bytes,
-                                           _ptr(dev_error), _stream(stream))
-    _check(st, "jl_bifocal_decode_paged")
+    _call(dev, lib().jl_bifocal_decode_paged, "jl_bifocal_decode_paged", q.data_ptr(), ctypes.byref(kv),
+          block_table.data_ptr(), M, seq_lens.data_ptr(), o.data_ptr(), _addr(lse), B, Hq, Hkv, D, int(w0), int(w_pretrained),
+          float(rope_base), float(softmax_scale), int(mode), _addr(workspace), ws_bytes, _addr(dev_error),
+          stream=stream)
 
 
 def jl_bifocal_decode_paged_sparse(q, k_pages, v_pages, block_table, seq_lens, page_list, page_counts, o, lse, *,
@@ -611,19 +649,16 @@ def jl_bifocal_decode_paged_sparse(q, k_pages, v_pages, block_table, seq_lens, p
                                    mode: int = JL_QSHIFT_SELF_EXTEND, workspace=None, dev_error=None, stream=None):
     """jl_bifocal_decode_paged over the pages that page_list int32 [B, Hkv, n] names (logical
     pages, the first page_counts[b, g] of each row; page_counts int32 [B, Hkv])."""
-    import torch
+    torch = _torch()
     B, Hq, Hkv, D, M, dev, kv, ws_bytes = _decode_paged_tensors(q, k_pages, v_pages, block_table, seq_lens, o, lse,
                                                                 workspace, dev_error)
     n = page_list.shape[2]
     _check_on(dev, ((page_list, "page_list", torch.int32, (B, Hkv, n)),
                     (page_counts, "page_counts", torch.int32, (B, Hkv))))
-    with _on_device(dev):
-        st = lib().jl_bifocal_decode_paged_sparse(_ptr(q), ctypes.byref(kv), _ptr(block_table), M, _ptr(seq_lens),
-                                                  _ptr(page_list), n, _ptr(page_counts), _ptr(o), _ptr(lse), B, Hq,
-                                                  Hkv, D, int(w0), int(w_pretrained), float(rope_base),
-                                                  float(softmax_scale), int(mode), _ptr(workspace), ws_bytes,
-                                                  _ptr(dev_error), _stream(stream))
-    _check(st, "jl_bifocal_decode_paged_sparse")
+    _call(dev, lib().jl_bifocal_decode_paged_sparse, "jl_bifocal_decode_paged_sparse", q.data_ptr(), ctypes.byref(kv),
+          block_table.data_ptr(), M, seq_lens.data_ptr(), page_list.data_ptr(), n, page_counts.data_ptr(), o.data_ptr(), _addr(lse), B,
+          Hq, Hkv, D, int(w0), int(w_pretrained), float(rope_base), float(softmax_scale), int(mode), _addr(workspace),
+          ws_bytes, _addr(dev_error), stream=stream)
 
 
 def jl_page_summaries(k_pages, block_table, starts, seq_lens, summaries, *, max_new: int, rope_base: float,
@@ -631,20 +666,18 @@ def jl_page_summaries(k_pages, block_table, starts, seq_lens, summaries, *, max_
     """Mean key of every page that holds positions starts[b] .. seq_lens[b] - 1 (int32 [B]) into
     summaries [num_pages, Hkv, D] (bf16, contiguous, indexed like the pages); max_new >= every
     seq_lens[b] - starts[b]."""
-    import torch
+    torch = _torch()
     B, M = block_table.shape
-    dev = k_pages.get_device()
+    dev = _device_of(k_pages, "k_pages")
     n, _, Hkv, D = k_pages.shape
     i32 = torch.int32
     _check_on(dev, ((block_table, "block_table", i32, (B, M)), (starts, "starts", i32, (B,)),
                     (seq_lens, "seq_lens", i32, (B,)), (summaries, "summaries", torch.bfloat16, (n, Hkv, D))))
-    _check_opt(dev, dev_error, "dev_error", i32, None)
+    _check_error_word(dev, dev_error)
     kv = _paged_kv(k_pages, None, dev)
-    with _on_device(dev):
-        st = lib().jl_page_summaries(ctypes.byref(kv), _ptr(block_table), M, _ptr(starts), _ptr(seq_lens),
-                                     int(max_new), _ptr(summaries), B, Hkv, D, float(rope_base), _ptr(dev_error),
-                                     _stream(stream))
-    _check(st, "jl_page_summaries")
+    _call(dev, lib().jl_page_summaries, "jl_page_summaries", ctypes.byref(kv), block_table.data_ptr(), M, starts.data_ptr(),
+          seq_lens.data_ptr(), int(max_new), summaries.data_ptr(), B, Hkv, D, float(rope_base), _addr(dev_error),
+          stream=stream)
 
 
 def jl_select_pages_workspace_bytes(B: int, Hkv: int, max_pages: int) -> int:
@@ -658,21 +691,19 @@ def jl_select_pages(q, summaries, block_table, seq_lens, page_list, page_counts,
     best by score, per KV head, ascending into page_list int32 [B, Hkv, n] (-1 behind them) and
     page_counts int32 [B, Hkv].  n >= min(max_pages, sink_pages + top_k + ceil(w0 / page_size) + 1);
     workspace: uint8 CUDA tensor of jl_select_pages_workspace_bytes(...) bytes."""
-    import torch
+    torch = _torch()
     B, Hq, D = q.shape
     num_pages, Hkv, _ = summaries.shape
     M = block_table.shape[1]
     n = page_list.shape[2]
-    dev = q.get_device()
+    dev = _device_of(q, "q")
     bf16, i32 = torch.bfloat16, torch.int32
-    _check_on(dev, ((q, "q", bf16, None), (summaries, "summaries", bf16, (num_pages, Hkv, D)),
+    _check_on(dev, ((q, "q", bf16, (B, Hq, D)), (summaries, "summaries", bf16, (num_pages, Hkv, D)),
                     (block_table, "block_table", i32, (B, M)), (seq_lens, "seq_lens", i32, (B,)),
                     (page_list, "page_list", i32, (B, Hkv, n)), (page_counts, "page_counts", i32, (B, Hkv))))
-    _check_opt(dev, dev_error, "dev_error", i32, None)
+    _check_error_word(dev, dev_error)
     ws_bytes = _workspace(dev, workspace)
-    with _on_device(dev):
-        st = lib().jl_select_pages(_ptr(q), _ptr(summaries), num_pages, int(page_size), _ptr(block_table), M,
-                                   _ptr(seq_lens), int(sink_pages), int(top_k), _ptr(page_list), n,
-                                   _ptr(page_counts), B, Hq, Hkv, D, int(w0), int(w_pretrained), float(rope_base),
-                                   int(mode), _ptr(workspace), ws_bytes, _ptr(dev_error), _stream(stream))
-    _check(st, "jl_select_pages")
+    _call(dev, lib().jl_select_pages, "jl_select_pages", q.data_ptr(), summaries.data_ptr(), num_pages, int(page_size),
+          block_table.data_ptr(), M, seq_lens.data_ptr(), int(sink_pages), int(top_k), page_list.data_ptr(), n,
+          page_counts.data_ptr(), B, Hq, Hkv, D, int(w0), int(w_pretrained), float(rope_base), int(mode),
+          _addr(workspace), ws_bytes, _addr(dev_error), stream=stream)
