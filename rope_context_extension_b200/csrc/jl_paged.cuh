@@ -36,10 +36,10 @@ struct NormRopeArgs {
   int64_t max_pages;
   int B;
   int T, Hq, Hkv;
-  int64_t heads_per_task;   // heads of one token that one warp handles (whole passes)
+  int heads_per_task;       // heads of one token that one warp handles (whole passes)
   int tasks_per_token;
   int* dev_error;
-  double u_hi[kMaxHalfDim], u_lo[kMaxHalfDim];
+  uint64_t turn[kMaxHalfDim];  // theta_t / 2 pi in 64-bit fixed point
 };
 cudaError_t launch_norm_rope(NormRopeArgs& a, int D, cudaStream_t stream);
 
@@ -82,7 +82,7 @@ struct PageSummaryArgs {
   int B, Hkv;
   int pages_per_seq;         // bound on the pages one sequence's new tokens touch
   int* dev_error;
-  double u_hi[kMaxHalfDim], u_lo[kMaxHalfDim];
+  uint64_t turn[kMaxHalfDim];  // theta_t / 2 pi in 64-bit fixed point
 };
 cudaError_t launch_page_summaries(const PageSummaryArgs& a, int D, cudaStream_t stream);
 
@@ -110,18 +110,6 @@ struct PageSelectArgs {
   uint64_t turn[kMaxHalfDim];      // theta_t / 2 pi in 64-bit fixed point
 };
 cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream);
-
-// cos and sin of n * theta (theta / 2 pi = u_hi + u_lo as sincos_int_angle takes
-// it): whole turns removed exactly in fp64, the rest in fp32.  The remainder, at
-// most half a turn, is rounded to fp32 once (2^-26 turns, 1e-7 rad), far inside
-// the bf16 rounding (2^-9) or the hi + lo split (2^-17) of what is rotated.
-__device__ __forceinline__ void sincos_turns(int64_t n, double u_hi, double u_lo, float* s, float* c) {
-  double a = (double)n * u_hi;  // exact for |n| < 2^31
-  a -= rint(a);
-  double f = a + (double)n * u_lo;
-  f -= rint(f);
-  sincospif(2.f * (float)f, s, c);
-}
 
 // cos and sin of n turns' worth of theta: turn = theta / 2 pi in 64-bit fixed
 // point, whole turns fall off the top.  The phase is good to 2^-31 turns plus

@@ -139,7 +139,7 @@ int norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, 
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.dev_error = dev_error;
-  set_turns(a, D, rope_base);
+  std::memcpy(a.turn, jl::turn_table(D, rope_base).fixed, sizeof(a.turn));
   if (jl::launch_norm_rope(a, D, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return JL_ERR_CUDA;
   return JL_OK;
 }
@@ -284,7 +284,7 @@ int jl_page_summaries(const jl_paged_kv* cache, const int32_t* block_table, int6
   a.pages_per_seq = (int)std::min<int64_t>(((int64_t)max_new + 2 * cache->page_size - 2) / cache->page_size,
                                            max_pages);
   a.dev_error = dev_error;
-  set_turns(a, head_dim, rope_base);
+  std::memcpy(a.turn, jl::turn_table(head_dim, rope_base).fixed, sizeof(a.turn));
   if (jl::launch_page_summaries(a, head_dim, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return JL_ERR_CUDA;
   return JL_OK;

@@ -39,29 +39,47 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   }
 }
 
-// One warp per (page, KV head).  A key row takes D/16 lanes of two 16-byte loads,
-// a warp reads 512 / D rows at a time, and each group of lanes sums its rows by
-// Horner's rule in R(-step): sum_i R(-step i) k_{step i + grp}, so that two fixed
-// rotations per lane, formed once per warp, serve every page.
+// cos and sin of n theta, theta / 2 pi in 64-bit fixed point as sincos_phase takes
+// it, the phase's sine and cosine to fp32.
+__device__ __forceinline__ void sincos_fixed(int n, uint64_t turn, float* s, float* c) {
+  const uint32_t m = (uint32_t)(n < 0 ? -n : n);
+  const uint32_t ph = m * (uint32_t)(turn >> 32) + __umulhi(m, (uint32_t)turn);
+  float sn;
+  sincospif((float)(int32_t)ph * 4.656612873077393e-10f, &sn, c);  // 2 / 2^32
+  *s = n < 0 ? -sn : sn;
+}
+
+// One warp per (page, KV head).  A key row takes D/16 lanes of two 16-byte loads, a
+// warp reads 512 / D rows at a time and kAhead such passes before it sums them, and
+// each group of lanes sums its rows by Horner's rule in R(-step): sum_i R(-step i)
+// k_{step i + grp}, so that two fixed rotations per lane, formed once per warp, serve
+// every page.  Memory bound: a page's keys are read once.
 template <int D>
-__global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm) page_summary_kernel(const __grid_constant__ PageSummaryArgs a) {
+__global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm)
+    page_summary_kernel(const __grid_constant__ PageSummaryArgs a) {
   constexpr int H2 = D / 2;
   constexpr int kLanes = D / 16;
   constexpr int kStep = 32 / kLanes;  // rows per pass
+  constexpr int kAhead = 4;
   const int lane = threadIdx.x & 31;
   const int sub = lane % kLanes, grp = lane / kLanes;
   const int P = a.pages.page_size;
   float sc[8], ss[8], mc[8], ms[8];  // R(-step), R(m - grp)
+  {
+    const uint64_t* tp = a.turn;  // a generic read: an indexed parameter read serialises
+    asm volatile("" : "+l"(tp));
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    sincos_turns(-kStep, a.u_hi[8 * sub + e], a.u_lo[8 * sub + e], &ss[e], &sc[e]);
-    sincos_turns(P / 2 - grp, a.u_hi[8 * sub + e], a.u_lo[8 * sub + e], &ms[e], &mc[e]);
+    for (int e = 0; e < 8; ++e) {
+      const uint64_t turn = tp[8 * sub + e];
+      sincos_fixed(-kStep, turn, &ss[e], &sc[e]);
+      sincos_fixed(P / 2 - grp, turn, &ms[e], &mc[e]);
+    }
   }
   const int64_t tasks = (int64_t)a.B * a.pages_per_seq * a.Hkv;
   const int64_t nwarps = (int64_t)gridDim.x * (kSumThreads / 32);
   for (int64_t task = ((int64_t)blockIdx.x * kSumThreads + threadIdx.x) >> 5; task < tasks; task += nwarps) {
-    const int g = (int)(task % a.Hkv);
     const int64_t bp = task / a.Hkv;
+    const int g = (int)(task - bp * a.Hkv);
     const int b = (int)(bp / a.pages_per_seq);
     const int i = (int)(bp - (int64_t)b * a.pages_per_seq);
     const int L = a.seq_lens[b], start = a.starts[b];
@@ -80,25 +98,34 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm) page_summary_ker
       continue;
     }
     const int n = min(P, L - lp * P);
-    const __nv_bfloat16* base = a.pages.k + phys * a.pages.page_stride + g * a.pages.head_stride;
+    const __nv_bfloat16* base =
+        a.pages.k + phys * a.pages.page_stride + g * a.pages.head_stride + grp * a.pages.row_stride + 8 * sub;
     float x[8], y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
-    for (int r0 = (n - 1) / kStep * kStep; r0 >= 0; r0 -= kStep) {
-      const int t = r0 + grp;
-      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-      if (t < n) {
-        lo = *reinterpret_cast<const uint4*>(base + t * a.pages.row_stride + 8 * sub);
-        hi = *reinterpret_cast<const uint4*>(base + t * a.pages.row_stride + H2 + 8 * sub);
-      }
-      float kx[8], ky[8];
-      unpack8(lo, kx);
-      unpack8(hi, ky);
+    for (int r0 = (n - 1) / kStep * kStep; r0 >= 0; r0 -= kAhead * kStep) {
+      uint4 lo[kAhead], hi[kAhead];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xr = kx[e] + (x[e] * sc[e] - y[e] * ss[e]);
-        y[e] = ky[e] + (y[e] * sc[e] + x[e] * ss[e]);
-        x[e] = xr;
+      for (int s = 0; s < kAhead; ++s) {
+        const int row = r0 - s * kStep;
+        lo[s] = hi[s] = make_uint4(0, 0, 0, 0);
+        if (row >= 0 && row + grp < n) {
+          lo[s] = *reinterpret_cast<const uint4*>(base + row * a.pages.row_stride);
+          hi[s] = *reinterpret_cast<const uint4*>(base + row * a.pages.row_stride + H2);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        if (r0 - s * kStep < 0) break;
+        float kx[8], ky[8];
+        unpack8(lo[s], kx);
+        unpack8(hi[s], ky);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float xr = kx[e] + (x[e] * sc[e] - y[e] * ss[e]);
+          y[e] = ky[e] + (y[e] * sc[e] + x[e] * ss[e]);
+          x[e] = xr;
+        }
       }
     }
     const float inv = 1.f / (float)n;

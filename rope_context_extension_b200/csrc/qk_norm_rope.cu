@@ -13,9 +13,10 @@
 // of a row's first half and the 8 that pair with them in the second (two 16-byte
 // loads), so a row takes D/16 lanes, the sum of squares takes log2(D/16)
 // shuffles, and no value crosses lanes for the rotation.  A warp handles 512 / D
-// rows at a time and a slice of one token's heads per task; the token's D/2
-// factors are formed once per task, two per lane (one for D = 64), and shared
-// through shared memory.
+// rows at a time, the next ones already on their way, and a slice of one token's
+// heads per task; the token's D/2 factors are formed once per task, two per lane,
+// and shared through shared memory (64-bit fixed-point angles and the MUFU's sine:
+// 2^-21, against the result's 2^-8).
 #include <algorithm>
 
 #include "jl_paged.cuh"
@@ -46,23 +47,40 @@ __global__ void __launch_bounds__(kNrThreads, kBlocksPerSm) norm_rope_kernel(con
   constexpr int H2 = D / 2;
   constexpr int kLanes = D / 16;       // lanes per head row
   constexpr int kRows = 32 / kLanes;   // head rows per pass of a warp
-  constexpr int kOwn = H2 / 32;        // angles a lane forms
-  __shared__ __align__(16) float2 cs_all[kNrThreads / 32][H2];
+  __shared__ __align__(16) float4 cs_all[kNrThreads / 32][H2 / 2];  // a token's factors (c, c, s, s)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float2* cs = cs_all[warp];
+  float4* cs = cs_all[warp];
   const int sub = lane % kLanes, grp = lane / kLanes;
-  double uh[kOwn], ul[kOwn];
-#pragma unroll
-  for (int e = 0; e < kOwn; ++e) {
-    uh[e] = a.u_hi[lane + 32 * e];
-    ul[e] = a.u_lo[lane + 32 * e];
+  // the pairs ft, ft + 1 whose factors this lane forms, where lanes of a row read them side by side
+  const int fl = lane % (H2 / 2), ft = 8 * (fl % kLanes) + 2 * (fl / kLanes);
+  uint64_t turn0, turn1;
+  {
+    const uint64_t* tp = a.turn;  // a generic read: an indexed parameter read serialises
+    asm volatile("" : "+l"(tp));
+    turn0 = tp[ft];
+    turn1 = tp[ft + 1];
   }
   const int heads = a.Hq + a.Hkv + (a.v != nullptr ? a.Hkv : 0);
   const int64_t tasks = (int64_t)a.T * a.tasks_per_token;
   const int64_t nwarps = (int64_t)gridDim.x * (kNrThreads / 32);
   for (int64_t task = (int64_t)blockIdx.x * (kNrThreads / 32) + warp; task < tasks; task += nwarps) {
-    const int64_t tok = task / a.tasks_per_token;
+    const int64_t tok = a.tasks_per_token == 1 ? task : task / a.tasks_per_token;
     const int slice = (int)(task - tok * a.tasks_per_token);
+    const int h0 = slice * a.heads_per_task, h1 = min(heads, h0 + a.heads_per_task);
+    // a pass's rows: loaded one pass ahead
+    uint4 lo, hi, next_lo, next_hi;
+    auto load = [&](int h) {
+      next_lo = next_hi = make_uint4(0, 0, 0, 0);
+      if (h < h1) {
+        const __nv_bfloat16* src = h < a.Hq ? a.q + tok * a.q_stride + (int64_t)h * D
+                                   : h < a.Hq + a.Hkv
+                                       ? a.k + tok * a.k_stride + (int64_t)(h - a.Hq) * D
+                                       : a.v + tok * a.v_stride + (int64_t)(h - a.Hq - a.Hkv) * D;
+        next_lo = *reinterpret_cast<const uint4*>(src + 8 * sub);
+        next_hi = *reinterpret_cast<const uint4*>(src + H2 + 8 * sub);
+      }
+    };
+    load(h0 + grp);
     const int pos = a.positions[tok];
     if (pos == -1) continue;  // a padded token
     bool bad = pos < 0;
@@ -71,42 +89,31 @@ __global__ void __launch_bounds__(kNrThreads, kBlocksPerSm) norm_rope_kernel(con
       const int sq = a.seq_ids[tok];
       bad = bad || sq < 0 || sq >= a.B || (int64_t)pos >= a.max_pages * a.pages.page_size;
       if (!bad) {
-        const int page = a.block_table[(int64_t)sq * a.max_pages + pos / a.pages.page_size];
+        const int lp = pos / a.pages.page_size;
+        const int page = a.block_table[(int64_t)sq * a.max_pages + lp];
         bad = page < 0 || page >= a.pages.num_pages;
-        kv_base = page * a.pages.page_stride + (int64_t)(pos % a.pages.page_size) * a.pages.row_stride;
+        kv_base = page * a.pages.page_stride + (int64_t)(pos - lp * a.pages.page_size) * a.pages.row_stride;
       }
     }
     if (bad) {
       if (lane == 0 && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
       continue;
     }
-    __syncwarp();
-#pragma unroll
-    for (int e = 0; e < kOwn; ++e) {
-      float s, c;
-      sincos_turns(pos, uh[e], ul[e], &s, &c);
-      cs[lane + 32 * e] = make_float2(c, s);
+    {
+      float4 f;
+      sincos_phase(pos, turn0, &f.z, &f.x);
+      sincos_phase(pos, turn1, &f.w, &f.y);
+      __syncwarp();
+      cs[fl] = f;
+      __syncwarp();
     }
-    __syncwarp();
-    float2 f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = cs[8 * sub + e];
-
-    const int h0 = (int)(slice * a.heads_per_task);
-    const int h1 = min(heads, (int)(h0 + a.heads_per_task));
     for (int hb = h0; hb < h1; hb += kRows) {
       const int h = hb + grp;
-      const bool live = h < h1;
+      lo = next_lo;
+      hi = next_hi;
+      load(h + kRows);
       const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
       const int hk = h - a.Hq - (is_v ? a.Hkv : 0);
-      const __nv_bfloat16* src = is_q   ? a.q + tok * a.q_stride + (int64_t)h * D
-                                 : is_v ? a.v + tok * a.v_stride + (int64_t)hk * D
-                                        : a.k + tok * a.k_stride + (int64_t)hk * D;
-      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-      if (live) {
-        lo = *reinterpret_cast<const uint4*>(src + 8 * sub);
-        hi = *reinterpret_cast<const uint4*>(src + H2 + 8 * sub);
-      }
       float x[8], y[8];
       bf16x8_to_f32(lo, x);
       bf16x8_to_f32(hi, y);
@@ -115,7 +122,7 @@ __global__ void __launch_bounds__(kNrThreads, kBlocksPerSm) norm_rope_kernel(con
       for (int e = 0; e < 8; ++e) ss += x[e] * x[e] + y[e] * y[e];
 #pragma unroll
       for (int m = 1; m < kLanes; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      if (!live) continue;
+      if (h >= h1) continue;
       if (!is_v) {
         const __nv_bfloat16* w = is_q ? a.qw : a.kw;
         if (w != nullptr) {
@@ -130,10 +137,13 @@ __global__ void __launch_bounds__(kNrThreads, kBlocksPerSm) norm_rope_kernel(con
           }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xr = x[e] * f[e].x - y[e] * f[e].y;
-          y[e] = y[e] * f[e].x + x[e] * f[e].y;
-          x[e] = xr;
+        for (int e = 0; e < 8; e += 2) {
+          const float4 f = cs[(e / 2) * kLanes + sub];
+          const float x0 = x[e] * f.x - y[e] * f.z, x1 = x[e + 1] * f.y - y[e + 1] * f.w;
+          y[e] = y[e] * f.x + x[e] * f.z;
+          y[e + 1] = y[e + 1] * f.y + x[e + 1] * f.w;
+          x[e] = x0;
+          x[e + 1] = x1;
         }
         lo = f32_to_bf16x8(x);
         hi = f32_to_bf16x8(y);
@@ -159,14 +169,19 @@ cudaError_t launch_d(NormRopeArgs& a, cudaStream_t stream) {
   if (sms == 0) return cudaErrorNoDevice;
   const int heads = a.Hq + a.Hkv + (a.v != nullptr ? a.Hkv : 0);
   const int passes = (heads + kRows - 1) / kRows;
-  // One pass of a warp per task while the tokens do not fill the GPU's warps (a
-  // decode step's latency); whole tokens per task (the factors formed once) when
-  // they do.
+  // Passes per task: what keeps the resident warps' last round full, counting two
+  // passes' time for a task's own start (position, page, factors).
   const int64_t warps = (int64_t)sms * kBlocksPerSm * (kNrThreads / 32);
-  int64_t per_task = ((int64_t)a.T * passes + warps - 1) / warps;
-  if (per_task > passes) per_task = passes;
-  a.heads_per_task = per_task * kRows;
-  a.tasks_per_token = (int)((passes + per_task - 1) / per_task);
+  int64_t best = INT64_MAX;
+  for (int per = 1; per <= passes; ++per) {
+    const int each = (passes + per - 1) / per;
+    const int64_t cost = (((int64_t)a.T * each + warps - 1) / warps) * (per + 2);
+    if (cost < best) {
+      best = cost;
+      a.heads_per_task = per * kRows;
+      a.tasks_per_token = each;
+    }
+  }
   const int64_t tasks = (int64_t)a.T * a.tasks_per_token;
   const int64_t blocks = std::min<int64_t>((tasks + kNrThreads / 32 - 1) / (kNrThreads / 32), (int64_t)sms * kBlocksPerSm);
   norm_rope_kernel<D><<<(unsigned)blocks, kNrThreads, 0, stream>>>(a);
