@@ -110,6 +110,28 @@ __device__ __forceinline__ void lds_u4(uint32_t addr, uint32_t (&v)[4]) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
 
+// Packed pair v = (a, b) -> bf16x2 hi = round(a, b) and the negated rest, lo = round(hi
+// - (a, b)), by the mixed subtraction that takes hi's halves as they are.
+__device__ __forceinline__ void split_neg_bf16(uint64_t v, uint32_t& hi, uint32_t& lo) {
+  float a, b, ra, rb;
+  f2_unpack(v, a, b);
+  hi = pack_bf16x2(a, b);
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tsub.rn.f32.bf16 %0, l, %3;\n\tsub.rn.f32.bf16 %1, h, %4;\n\t}"
+      : "=f"(ra), "=f"(rb)
+      : "r"(hi), "f"(a), "f"(b));
+  lo = pack_bf16x2(ra, rb);
+}
+
+// The bf16 pairs (x, y) of two adjacent RoPE pairs turned by f = (c0, c1, s0, s1), as
+// hi parts and negated lo parts.
+__device__ __forceinline__ void rot_split_neg(uint32_t xw, uint32_t yw, const float4& f, uint32_t& xh, uint32_t& xl,
+                                              uint32_t& yh, uint32_t& yl) {
+  const uint64_t x = bf16x2_to_f2(xw), y = bf16x2_to_f2(yw);
+  const uint64_t c = f2_pack(f.x, f.y), sn = f2_pack(f.z, f.w);
+  split_neg_bf16(f2_sub(f2_mul(x, c), f2_mul(y, sn)), xh, xl);
+  split_neg_bf16(f2_fma(x, sn, f2_mul(y, c)), yh, yl);
+}
+
 // B fragments of k-step ks for the unit's 16 keys; tile: the lane's place in the unit's keys.
 template <int D>
 __device__ __forceinline__ void load_keys(uint32_t tile, int ks, uint32_t (&k)[4]) {
@@ -170,6 +192,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   Entry* ent = reinterpret_cast<Entry*>(smem + C::kEntOff);  // the warps' heads (2 w) and tails (2 w + 1)
 
   bool any_empty;
+  if (tid == 0) {
+    tma_prefetch_map(&tm_k);
+    tma_prefetch_map(&tm_v);
+  }
   // ---- how much there is to do, and where this CTA's and this warp's share is
   const int per_seg = (items + kSegs - 1) / kSegs;
   if (tid < kWarps * S) mbar_init(smem_addr(smem + C::kBarOff) + 8 * tid, 1);
@@ -360,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The output of head 2 c4 + (k & 1), dim 16 mt + hrow + (k & 2 ? 8 : 0).
   auto out_value = [&](int mt, int k) {
     float v = oacc[mt][k];
-    if (kPack) v += __shfl_down_sync(0xffffffffu, v, 2);  // + the lo parts' product, four columns on
+    if (kPack) v -= __shfl_down_sync(0xffffffffu, v, 2);  // + the lo parts' product (negated), four columns on
     return v;
   };
   // Writes the warp's accumulated segment as a partial (m, l, o).
@@ -522,8 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               q0 = qf[i][0], q1 = qf[i][1], q2 = qf[i + KS2][0], q3 = qf[i + KS2][1];
             }
             uint4 lo, hi;
-            rot_split_bf16(q0, q2, csb[8 * kp + c4], lo.x, lo.y, hi.x, hi.y);
-            rot_split_bf16(q1, q3, csb[8 * kp + 4 + c4], lo.z, lo.w, hi.z, hi.w);
+            rot_split_neg(q0, q2, csb[8 * kp + c4], lo.x, lo.y, hi.x, hi.y);
+            rot_split_neg(q1, q3, csb[8 * kp + 4 + c4], lo.z, lo.w, hi.z, hi.w);
             qbuf[(kp * 2) * kQLanes + qlane] = lo;
             qbuf[(kp * 2 + 1) * kQLanes + qlane] = hi;
           }
@@ -546,8 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // This lane's scores: keys 8 nt + 2 c4 + {0, 1} of head hq.  A unit on the
         // band's edge forms both kinds and each key keeps its own.
         if (any_remote) {
-          // hi and lo parts of the keys in accumulators of their own, of the queries in
-          // rows h and h + 8: the sum of all four is (q_hi + q_lo) . (k_hi + k_lo)
+          // hi and (negated) lo parts of the keys in accumulators of their own, of the
+          // queries in rows h and h + 8: the four add up to (q_hi + q_lo) . (k_hi + k_lo)
           float sah[2][4], sal[2][4];
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt)
@@ -567,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               float4 f01, f23;
               lds_f4(ef[nt] + kp * 128, f01);
               lds_f4(ef[nt] + kp * 128 + 64, f23);
-              rot_split_bf16(klo[2 * nt], khi[2 * nt], f01, kah[2 * nt], kal[2 * nt], kbh[2 * nt], kbl[2 * nt]);
-              rot_split_bf16(klo[2 * nt + 1], khi[2 * nt + 1], f23, kah[2 * nt + 1], kal[2 * nt + 1],
+              rot_split_neg(klo[2 * nt], khi[2 * nt], f01, kah[2 * nt], kal[2 * nt], kbh[2 * nt], kbl[2 * nt]);
+              rot_split_neg(klo[2 * nt + 1], khi[2 * nt + 1], f23, kah[2 * nt + 1], kal[2 * nt + 1],
                              kbh[2 * nt + 1], kbl[2 * nt + 1]);
             }
 #pragma unroll
@@ -583,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              x[nt][e] = (sah[nt][e] + sah[nt][e + 2]) + (sal[nt][e] + sal[nt][e + 2]);
+              x[nt][e] = (sah[nt][e] - sah[nt][e + 2]) - (sal[nt][e] - sal[nt][e + 2]);
         }
         if (any_local) {  // base query, keys as stored
           float sb[2][4];
@@ -645,7 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int nt = 0; nt < 2; ++nt) {
           const float p0 = ex2_approx(x[nt][0] - msub), p1 = ex2_approx(x[nt][1] - msub);
           l_part += p0 + p1;
-          split_f2_bf16(f2_pack(p0, p1), ph[nt], pl[nt]);
+          if (kPack)
+            split_neg_bf16(f2_pack(p0, p1), ph[nt], pl[nt]);
+          else
+            split_f2_bf16(f2_pack(p0, p1), ph[nt], pl[nt]);
         }
         const uint32_t pb0 = kPack && hrow >= 4 ? pl[0] : ph[0];
         const uint32_t pb1 = kPack && hrow >= 4 ? pl[1] : ph[1];
@@ -712,10 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int it = ent[e].item;
     if (it < 0 || it == done) continue;
     done = it;
-    int head = -1;  // the warp whose head this item is
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (ent[2 * w].item == it) head = w;
+    const unsigned heads = __ballot_sync(0xffffffffu, lane < kWarps && ent[2 * lane].item == it);
+    const int head = heads ? __ffs(heads) - 1 : -1;  // the warp whose head this item is
     const int64_t s = ent[e].s;
     const bool whole = s >= c0 && s + ent[e].n <= c1;
     const int slot = s < c0 ? 0 : 1;
@@ -726,28 +753,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const Partial out = partial_at(a.cta_parts, (int64_t)blockIdx.x * 2 + slot, part_floats);
     const Partial hp = partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + (head < 0 ? 0 : head), part_floats);
-    static_assert(kMaxR * D / 4 <= kThreads, "one step of the loop below");
-    for (int idx = 4 * tid; idx < r * D; idx += 4 * kThreads) {
-      const int h = idx / D;
-      float m[kWarps + 1], l[kWarps + 1], M = -INFINITY;
+    // A warp joins 128 values, four per lane.  Lanes 0 .. 12 of either half hold the
+    // parts' weights for the half's head.  (Rolled loops: this code runs once per CTA,
+    // and unrolled it is its fetch that takes the time.)
+    static_assert(kWarps < 16 && D >= 64, "one part per lane, at most two heads per warp");
+#pragma unroll 1
+    for (int base = 128 * warp; base < r * D; base += 128 * kWarps) {
+      const int idx = base + 4 * lane;
+      const int h = min(idx / D, r - 1);
+      const int w = lane & 15;
+      const bool in = w < kWarps ? ent[2 * w + 1].item == it : (w == kWarps && head >= 0);
+      const Partial p = w < kWarps ? partial_at(reinterpret_cast<float*>(smem), w, S * C::kSlot / 4) : hp;
+      const float m = in ? p.m[h] : -INFINITY, l = in ? p.l[h] : 0.f;
+      float M = m;
 #pragma unroll
-      for (int w = 0; w <= kWarps; ++w) {
-        const Partial p = w < kWarps ? partial_at(reinterpret_cast<float*>(smem), w, S * C::kSlot / 4) : hp;
-        const bool in = w < kWarps ? ent[2 * w + 1].item == it : head >= 0;
-        m[w] = in ? p.m[h] : -INFINITY;
-        l[w] = in ? p.l[h] : 0.f;
-        M = fmaxf(M, m[w]);
-      }
+      for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float wt = weight(m, l, M);
+      float lsum = wt * l;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float lsum = 0.f;
-#pragma unroll
-      for (int w = 0; w <= kWarps; ++w) {
-        const Partial p = w < kWarps ? partial_at(reinterpret_cast<float*>(smem), w, S * C::kSlot / 4) : hp;
-        const bool in = w < kWarps ? ent[2 * w + 1].item == it : head >= 0;
-        const float wt = weight(m[w], l[w], M);
-        if (in) add(o, wt, *reinterpret_cast<const float4*>(p.o + idx));  // (a ring without a part holds anything)
-        lsum += wt * l[w];
+      unsigned parts = __ballot_sync(0xffffffffu, in) & 0xffffu;
+#pragma unroll 1
+      for (; parts != 0; parts &= parts - 1) {
+        const int c = __ffs(parts) - 1;
+        const float wc = __shfl_sync(0xffffffffu, wt, c, 16);
+        const Partial q = c < kWarps ? partial_at(reinterpret_cast<float*>(smem), c, S * C::kSlot / 4) : hp;
+        if (idx < r * D) add(o, wc, *reinterpret_cast<const float4*>(q.o + idx));
       }
+      if (idx >= r * D) continue;
       if (whole) {
         write_result(row_of(it), idx, o, M, lsum);
       } else {
