@@ -53,7 +53,11 @@ constexpr int kSegs = 128;  // runs of items whose unit counts the CTA scans
 #endif
 constexpr int kWarps = JL_PG_WARPS;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMinUnits = 2 * kWarps;  // units per CTA below which fewer CTAs share a call's work
+constexpr int kMinUnits = kWarps;  // units per CTA below which fewer CTAs share a call's work
+// Items that warps take whole: up to 4 units always, up to 8 where there are at least
+// two per CTA (measured: 512 items of 7 units 27.5 -> 22.6 us, 8 items of 8 units 16.4
+// -> 21.0 us).
+constexpr int kWholeUnits = 4, kWholeUnitsMany = 8;
 constexpr int kMaxR = 8;
 
 template <int D>
@@ -108,6 +112,15 @@ __device__ __forceinline__ void lds_f4(uint32_t addr, float4& f) {
 
 __device__ __forceinline__ void lds_u4(uint32_t addr, uint32_t (&v)[4]) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
+}
+
+// The first product of a sum.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Packed pair v = (a, b) -> bf16x2 hi = round(a, b) and the negated rest, lo = round(hi
@@ -183,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* scan = reinterpret_cast<int64_t*>(smem + C::kScanOff);
   volatile int* misc = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
   volatile int* abort_flag = misc;               // [0]
-  volatile int* ticket = misc + 1;               // [1]
+  volatile int* ticket = misc + 1;               // [1], [2]: whether this CTA joins the item it shares
   struct Entry {
     int64_t s;  // the item's first unit
     int n;      // its units
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   Entry* ent = reinterpret_cast<Entry*>(smem + C::kEntOff);  // the warps' heads (2 w) and tails (2 w + 1)
 
-  bool any_empty;
+  bool any_empty, any_large;
   if (tid == 0) {
     tma_prefetch_map(&tm_k);
     tma_prefetch_map(&tm_v);
@@ -207,11 +220,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < 2 * kWarps) ent[tid].item = -1;
   {
     int64_t v = 0;
-    bool none = false;
+    bool none = false, large = false;
+    const int whole_units = items >= 2 * (int)gridDim.x ? kWholeUnitsMany : kWholeUnits;
     if (tid < kSegs) {
       for (int i = tid * per_seg; i < items && i < (tid + 1) * per_seg; ++i) {
         const int n = item_units(a, i);
         none = none || n == 0;
+        large = large || n > whole_units;
         v += n;
       }
 #pragma unroll
@@ -222,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       scan[tid + 1] = v;
     }
     any_empty = __syncthreads_or(none);
+    any_large = __syncthreads_or(large);
     int64_t before = 0;
     if (tid < kSegs)
       for (int w = 0; w < warp; ++w) before += scan[32 * w + 32];
@@ -245,17 +261,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  const int64_t want = (U + kMinUnits - 1) / kMinUnits;
-  const int64_t N = want < gridDim.x ? want : gridDim.x;  // CTAs that share the line
-  if (blockIdx.x >= N) return;
-  const int64_t c0 = (int64_t)blockIdx.x * U / N, c1 = ((int64_t)blockIdx.x + 1) * U / N;
-  const int64_t wb = c0 + warp * (c1 - c0) / kWarps, we = c0 + (warp + 1) * (c1 - c0) / kWarps;
+  // CTAs that share the line, the CTA's stretch of it and the warp's.  Where every item
+  // is small (a batch of short sequences) warps take whole items instead, each counting
+  // its units from 0: a join costs more than the few units that this leaves uneven.
+  int64_t N, c0 = 0, c1 = 0, wb = 0, we = 0;
+  int first_item = 0;
+  if (any_large) {
+    const int64_t want = (U + kMinUnits - 1) / kMinUnits;
+    N = want < gridDim.x ? want : gridDim.x;
+    if (blockIdx.x >= N) return;
+    c0 = (int64_t)blockIdx.x * U / N;
+    c1 = ((int64_t)blockIdx.x + 1) * U / N;
+    wb = c0 + warp * (c1 - c0) / kWarps;
+    we = c0 + (warp + 1) * (c1 - c0) / kWarps;
+  } else {
+    N = min((items + kWarps - 1) / kWarps, (int)gridDim.x);
+    if (blockIdx.x >= N || U == 0) return;
+    const int64_t w = (int64_t)blockIdx.x * kWarps + warp, all = N * kWarps;
+    first_item = (int)(w * items / all);
+    const int last_item = (int)((w + 1) * items / all);
+    int n = 0;
+    for (int i = first_item + lane; i < last_item; i += 32) n += item_units(a, i);
+    we = __reduce_add_sync(0xffffffffu, n);
+  }
   const int cnt = (int)(we - wb);
 
   // ---- the walk over units: lane l holds the description of unit 32 * batch + l
-  int cur_it = 0;
+  int cur_it = first_item;
   int64_t cur_s = 0;  // cur_it: an item at or before the batch's first unit; cur_s: its first unit
-  if (cnt > 0) {
+  if (cnt > 0 && any_large) {
     // the run of items that holds unit wb, found by all lanes together
     int seg = 0;
     for (int t0 = 0; t0 < kSegs; t0 += 32) {
@@ -576,10 +610,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           // queries in rows h and h + 8: the four add up to (q_hi + q_lo) . (k_hi + k_lo)
           float sah[2][4], sal[2][4];
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sah[nt][e] = sal[nt][e] = 0.f;
-#pragma unroll
           for (int kp = 0; kp < KS2; ++kp) {
             // k-step kp holds the first coordinate of pairs t in [16 kp, 16 kp + 16), k-step
             // kp + D/32 the second, so each pair is complete in registers
@@ -599,8 +629,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-              mma_bf16(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
-              mma_bf16(sal[nt], alo, kal[2 * nt], kal[2 * nt + 1]);
+              if (kp == 0) {
+                mma_bf16_first(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
+                mma_bf16_first(sal[nt], alo, kal[2 * nt], kal[2 * nt + 1]);
+              } else {
+                mma_bf16(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
+                mma_bf16(sal[nt], alo, kal[2 * nt], kal[2 * nt + 1]);
+              }
               mma_bf16(sah[nt], ahi, kbh[2 * nt], kbh[2 * nt + 1]);
               mma_bf16(sal[nt], ahi, kbl[2 * nt], kbl[2 * nt + 1]);
             }
@@ -732,56 +767,66 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // A part's weight 2^(m - M): an empty part's sum is 0, and a NaN that left the maximum at -inf goes through.
   auto weight = [](float m, float l, float M) { return m == -INFINITY ? l : ex2_approx(m - M); };
-  int shared_item[2] = {-1, -1};  // items shared with the CTAs before and behind
-  int shared_n[2] = {0, 0};
-  int64_t shared_s[2] = {0, 0};
-  int done = -1;
+  static_assert(2 * kWarps <= 32 && kWarps < 16 && D >= 64, "entries in lanes; a part per lane of half a warp");
+  // lane e holds entry e: heads at 2 w, tails at 2 w + 1
+  const int my_item = lane < 2 * kWarps ? ent[lane].item : -1;
+  const int64_t my_s = lane < 2 * kWarps ? ent[lane].s : 0;
+  const int my_n = lane < 2 * kWarps ? ent[lane].n : 0;
+  const unsigned my_parts = __match_any_sync(0xffffffffu, my_item);  // entries of the same item
+  const bool my_whole = my_s >= c0 && my_s + my_n <= c1;
+  const bool my_first = my_item >= 0 && (my_parts & ((1u << lane) - 1u)) == 0u;
+  const unsigned firsts = __ballot_sync(0xffffffffu, my_first);
+  int shared_item[2], shared_n[2];  // items shared with the CTAs before and behind
+  int64_t shared_s[2];
+#pragma unroll
+  for (int slot = 0; slot < 2; ++slot) {
+    const unsigned m = __ballot_sync(0xffffffffu, my_first && !my_whole && (my_s < c0) == (slot == 0));
+    const int e = m ? __ffs(m) - 1 : 0;
+    shared_item[slot] = m ? __shfl_sync(0xffffffffu, my_item, e) : -1;
+    shared_n[slot] = __shfl_sync(0xffffffffu, my_n, e);
+    shared_s[slot] = __shfl_sync(0xffffffffu, my_s, e);
+  }
+  // A warp joins 128 values of an item, four per lane; lanes 0 .. 12 of either half hold
+  // the parts' weights for the half's head.  (Rolled loops: this code runs once per CTA,
+  // and unrolled it is its fetch that takes the time.)
+  const int blocks = (r * D + 127) / 128;
 #pragma unroll 1
-  for (int e = 0; e < 2 * kWarps; ++e) {  // heads at 2 w, tails at 2 w + 1
-    const int it = ent[e].item;
-    if (it < 0 || it == done) continue;
-    done = it;
-    const unsigned heads = __ballot_sync(0xffffffffu, lane < kWarps && ent[2 * lane].item == it);
-    const int head = heads ? __ffs(heads) - 1 : -1;  // the warp whose head this item is
-    const int64_t s = ent[e].s;
-    const bool whole = s >= c0 && s + ent[e].n <= c1;
-    const int slot = s < c0 ? 0 : 1;
-    if (!whole) {
-      shared_item[slot] = it;
-      shared_s[slot] = s;
-      shared_n[slot] = ent[e].n;
-    }
+  for (int t = warp; t < __popc(firsts) * blocks; t += kWarps) {
+    const int run = t / blocks;
+    unsigned rest = firsts;
+    for (int i = 0; i < run; ++i) rest &= rest - 1;
+    const int e = __ffs(rest) - 1;
+    const int it = __shfl_sync(0xffffffffu, my_item, e);
+    const unsigned entries = __shfl_sync(0xffffffffu, my_parts, e);
+    const bool whole = __shfl_sync(0xffffffffu, my_whole, e);
+    const int slot = __shfl_sync(0xffffffffu, my_s < c0, e) ? 0 : 1;
+    const unsigned heads = entries & 0x55555555u;
+    const int head = heads ? (__ffs(heads) - 1) >> 1 : 0;  // the warp whose head the item is, if one
     const Partial out = partial_at(a.cta_parts, (int64_t)blockIdx.x * 2 + slot, part_floats);
-    const Partial hp = partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + (head < 0 ? 0 : head), part_floats);
-    // A warp joins 128 values, four per lane.  Lanes 0 .. 12 of either half hold the
-    // parts' weights for the half's head.  (Rolled loops: this code runs once per CTA,
-    // and unrolled it is its fetch that takes the time.)
-    static_assert(kWarps < 16 && D >= 64, "one part per lane, at most two heads per warp");
-#pragma unroll 1
-    for (int base = 128 * warp; base < r * D; base += 128 * kWarps) {
-      const int idx = base + 4 * lane;
-      const int h = min(idx / D, r - 1);
-      const int w = lane & 15;
-      const bool in = w < kWarps ? ent[2 * w + 1].item == it : (w == kWarps && head >= 0);
-      const Partial p = w < kWarps ? partial_at(reinterpret_cast<float*>(smem), w, S * C::kSlot / 4) : hp;
-      const float m = in ? p.m[h] : -INFINITY, l = in ? p.l[h] : 0.f;
-      float M = m;
+    const Partial hp = partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + head, part_floats);
+    const int idx = 128 * (t - run * blocks) + 4 * lane;
+    const int h = min(idx / D, r - 1);
+    const int w = lane & 15;
+    const bool in = w < kWarps ? (entries >> (2 * w + 1)) & 1u : (w == kWarps && heads != 0u);
+    const Partial p = w < kWarps ? partial_at(reinterpret_cast<float*>(smem), w, S * C::kSlot / 4) : hp;
+    const float m = in ? p.m[h] : -INFINITY, l = in ? p.l[h] : 0.f;
+    float M = m;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float wt = weight(m, l, M);
-      float lsum = wt * l;
+    for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float wt = weight(m, l, M);
+    float lsum = wt * l;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      unsigned parts = __ballot_sync(0xffffffffu, in) & 0xffffu;
+    for (int o = 8; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    unsigned parts = __ballot_sync(0xffffffffu, in) & 0xffffu;
 #pragma unroll 1
-      for (; parts != 0; parts &= parts - 1) {
-        const int c = __ffs(parts) - 1;
-        const float wc = __shfl_sync(0xffffffffu, wt, c, 16);
-        const Partial q = c < kWarps ? partial_at(reinterpret_cast<float*>(smem), c, S * C::kSlot / 4) : hp;
-        if (idx < r * D) add(o, wc, *reinterpret_cast<const float4*>(q.o + idx));
-      }
-      if (idx >= r * D) continue;
+    for (; parts != 0; parts &= parts - 1) {
+      const int c = __ffs(parts) - 1;
+      const float wc = __shfl_sync(0xffffffffu, wt, c, 16);
+      const Partial q = c < kWarps ? partial_at(reinterpret_cast<float*>(smem), c, S * C::kSlot / 4) : hp;
+      if (idx < r * D) add(o, wc, *reinterpret_cast<const float4*>(q.o + idx));
+    }
+    if (idx < r * D) {
       if (whole) {
         write_result(row_of(it), idx, o, M, lsum);
       } else {
@@ -792,28 +837,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    __syncwarp();
   }
+  if (shared_item[0] < 0 && shared_item[1] < 0) return;  // the same for every thread of the CTA
 
   // ---- join the CTAs' partials: the item's last ticket does it
   float* wts = reinterpret_cast<float*>(smem + C::kWtsOff);  // [r][kMaxParts]
   float* part_l = wts + kMaxR * C::kMaxParts;                 // [r][kMaxParts] the parts' sums
   float* tot = part_l + kMaxR * C::kMaxParts;                 // [r] maxima, then [r] sums
   auto cta_of = [&](int64_t unit) -> int { return (int)(((unit + 1) * N - 1) / U); };
+  __threadfence();
+  __syncthreads();
+  if (tid < 2 && (tid == 0 ? shared_item[0] : shared_item[1]) >= 0) {
+    const int64_t s = tid == 0 ? shared_s[0] : shared_s[1];
+    const int first = cta_of(s), behind = cta_of(s + (tid == 0 ? shared_n[0] : shared_n[1]) - 1) - first;
+    ticket[tid] = atomicInc(&a.counters[first], (unsigned)behind) == (unsigned)behind;
+  }
+  __syncthreads();
 #pragma unroll 1
   for (int slot = 0; slot < 2; ++slot) {
     const int it = shared_item[slot];
-    if (it < 0) continue;  // the same for every thread of the CTA
+    if (it < 0 || ticket[slot] == 0) continue;  // the same for every thread of the CTA
     const int first = cta_of(shared_s[slot]), last = cta_of(shared_s[slot] + shared_n[slot] - 1);
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) *ticket = atomicInc(&a.counters[first], (unsigned)(last - first)) == (unsigned)(last - first);
-    __syncthreads();
-    if (*ticket == 0) continue;
     __threadfence();
     const int n = last - first + 1;
     // the item begins inside the first CTA's range (slot 1) and before the others' (slot 0)
     const int64_t step = 2 * part_floats;
     const float* parts = a.cta_parts + first * step;
+    // Thread groups take every groups-th part of four dims, then their sums meet in unit
+    // order; the first parts are on their way while the weights are formed.
+    const int cols = r * D / 4, groups = kThreads / cols;
+    const int grp = tid / cols, idx = 4 * (tid - grp * cols);
+    const float* po = parts + 2 * kMaxR + idx;
+    constexpr int kEarly = 4;
+    float4 early[kEarly];
+#pragma unroll
+    for (int i = 0; i < kEarly; ++i) {
+      const int c = grp + i * groups;
+      early[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (grp < groups && c < n)
+        early[i] = __ldcg(reinterpret_cast<const float4*>(po + c * step + (c == 0 ? part_floats : 0)));
+    }
     for (int h = warp; h < r; h += kWarps) {  // weights, one warp per head
       float* w = wts + h * C::kMaxParts;
       float M = -INFINITY, l = 0.f;
@@ -839,17 +903,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncthreads();
-    // thread groups take every groups-th part of four dims, then their sums meet in unit order
-    const int cols = r * D / 4, groups = kThreads / cols;
-    const int grp = tid / cols, idx = 4 * (tid - grp * cols);
     float4* sums = reinterpret_cast<float4*>(smem);  // [groups][cols]; the rings are done with
     if (grp < groups) {
       const float* w = wts + (idx / D) * C::kMaxParts;
-      const float* po = parts + 2 * kMaxR + idx;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kEarly; ++i)
+        if (grp + i * groups < n) add(o, w[grp + i * groups], early[i]);
 #pragma unroll 4
-      for (int c = grp; c < n; c += groups)
-        add(o, w[c], __ldcg(reinterpret_cast<const float4*>(po + c * step + (c == 0 ? part_floats : 0))));
+      for (int c = grp + kEarly * groups; c < n; c += groups)
+        add(o, w[c], __ldcg(reinterpret_cast<const float4*>(po + c * step)));
       sums[grp * cols + idx / 4] = o;
     }
     __syncthreads();
