@@ -531,10 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < D / 16; ++n) oacc[n][0] = oacc[n][1] = oacc[n][2] = oacc[n][3] = 0.f;
         const int b = item / a.Hkv, g = item - b * a.Hkv;
         L = a.seq_lens[b];
-        G = (int)group_size(L, a.w_pretrained);
+        // (group_size, query_remote and query_shift in 32 bits; 64-bit divisions are what a
+        // segment's start would spend its time on)
+        G = (int)((unsigned)(L - 1) / (unsigned)a.w_pretrained) + 1;
         all_local = jl::all_local(L, a.w0, G);
-        dq = (int)(query_remote(L - 1, G, query_shift(a.w0, G, a.qshift)) - (L - 1));
-        g_inv = (uint32_t)(((uint64_t)1 << 32) / (uint64_t)(G > 1 ? G : 2));
+        dq = all_local ? 0 : (L - 1) / G + (a.qshift == 1 ? a.w0 - a.w0 / G : 0) - (L - 1);
+        g_inv = 0xffffffffu / (unsigned)G;
         jb = -1;
         local_from = all_local ? 0 : L - a.w0;  // keys j >= local_from are scored with base RoPE
         const __nv_bfloat16* qp = a.q + ((int64_t)b * a.Hq + g * r + hq) * D + 2 * c4;
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any_remote = !all_local && j0 < local_from;
       uint32_t ef[2] = {0u, 0u};  // factor rows of this lane's keys hrow and 8 + hrow
       if (j0 >= 0 && any_remote) {
-        // floor(j0 / G) by the reciprocal rounded down (at most one short)
+        // floor(j0 / G) by floor((2^32 - 1) / G): at most one short
         int qd = (int)__umulhi((unsigned)j0, g_inv), rm = j0 - qd * G;
         if (rm >= G) {
           rm -= G;

@@ -460,22 +460,22 @@ def jl_wait_timeout_check(dev_error, timeout_s: float = 0.2, stream=None):
 # [num_pages, Hkv, page_size, D] pool, or the two halves of one pool); every
 # tensor of a call lives on the same device, which need not be the current one.
 # ---------------------------------------------------------------------------
+def _refuse(dev, t, name, dtype, shape):
+    """Raise for a tensor that failed the tests of _check_on, saying which."""
+    _check_tensor(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
 def _check_on(dev, specs):
     """specs: (tensor, name, dtype, shape) of contiguous tensors on device dev.  (One pass of
     cheap tests: a decode step's calls are as long as their host side.)"""
     for t, name, dtype, shape in specs:
         try:
-            ok = t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+            if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+                continue
         except AttributeError:
-            ok = False
-        if not ok:
-            _check_tensor(t, name, dtype, shape)
-            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-
-
-def _check_opt(dev, t, name, dtype, shape):
-    if t is not None:
-        _check_on(dev, ((t, name, dtype, shape),))
+            pass
+        _refuse(dev, t, name, dtype, shape)
 
 
 def _device_of(t, name):
@@ -488,64 +488,59 @@ def _device_of(t, name):
     return dev
 
 
-def _check_error_word(dev, t):
-    if t is not None:
-        _check_on(dev, ((t, "dev_error", _torch().int32, t.shape),))
-
-
-def _head_rows(t, name, T, H, D, dev):
+def _head_rows(dev, bf16, t, name, T, H, D):
     """Token stride of a [T, H, D] bf16 view whose heads are contiguous."""
-    if _device_of(t, name) != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    if t.dtype is not _torch().bfloat16:
-        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.shape != (T, H, D):
+    try:
+        st = t.stride()
+        if t.dtype is bf16 and t.shape == (T, H, D) and t.get_device() == dev:
+            if st[2] != 1 or (st[1] != D and H > 1):
+                raise ValueError(f"{name}: a token's heads must be contiguous")
+            return st[0] if T > 1 else H * D
+    except AttributeError:
+        pass
+    if _device_of(t, name) == dev and t.dtype is bf16:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H, D)}")
-    st = t.stride()
-    if st[2] != 1 or (H > 1 and st[1] != D):
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    return st[0] if T > 1 else H * D
+    raise ValueError(f"{name} must be torch.bfloat16 on cuda:{dev}, got {t.dtype} on {t.device}")
 
 
-def _paged_kv(k_pages, v_pages, dev, heads=None, head_dim=None):
-    bf16 = _torch().bfloat16
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if t is None and name == "v_pages":
-            continue
-        if _device_of(t, name) != dev:
-            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-        if t.dtype is not bf16:
-            raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        if t.dim() != 4 or t.stride(3) != 1:
-            raise ValueError(f"{name} must be [num_pages, page_size, Hkv, D] with contiguous rows")
+def _paged_kv(dev, bf16, k_pages, v_pages, head_dim=None):
+    """The jl_paged_kv of two [num_pages, page_size, Hkv, D] views; v_pages None: not used."""
+    if _device_of(k_pages, "k_pages") != dev or k_pages.dtype is not bf16:
+        raise ValueError(f"k_pages must be torch.bfloat16 on cuda:{dev}, got {k_pages.dtype} on {k_pages.device}")
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be [num_pages, page_size, Hkv, D]")
     n, P, H, D = k_pages.shape
-    if heads is not None and (H, D) != (heads, head_dim):
-        raise ValueError(f"k_pages holds {H} heads of {D}, expected {heads} of {head_dim}")
-    sp, sr, sh, _ = k_pages.stride()
-    if v_pages is not None and (v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride()):
-        raise ValueError("k_pages and v_pages must have the same shape and strides")
+    sp, sr, sh, one = strides = k_pages.stride()
+    if one != 1:
+        raise ValueError("k_pages must have contiguous rows")
+    if head_dim is not None and head_dim != D:
+        raise ValueError(f"k_pages holds rows of {D}, expected {head_dim}")
+    v = 0
+    if v_pages is not None:
+        if _device_of(v_pages, "v_pages") != dev or v_pages.dtype is not bf16:
+            raise ValueError(f"v_pages must be torch.bfloat16 on cuda:{dev}, got {v_pages.dtype} on {v_pages.device}")
+        if v_pages.shape != k_pages.shape or v_pages.stride() != strides:
+            raise ValueError("k_pages and v_pages must have the same shape and strides")
+        v = v_pages.data_ptr()
     if H == 1:  # a dimension of one has no stride of its own
         sh = D
     if n == 1:
         sp = (P - 1) * sr + (H - 1) * sh + D
         sp += -sp % 8
-    return _PagedKV(k_pages.data_ptr(), 0 if v_pages is None else v_pages.data_ptr(), n, sp, sr, sh, P)
+    return _PagedKV(k_pages.data_ptr(), v, n, sp, sr, sh, P)
 
 
 def _call(dev, fn, where, *args, stream=None):
     """fn(*args, stream) with device dev current and the caller's stream, or the current one of dev.
     (The two private getters are what torch's own generated launchers call: 0.1 us each, against
     1.5 us for a Stream object.)"""
-    c = _torch()._C
+    c = _torch_module._C
+    stream = c._cuda_getCurrentRawStream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
     if c._cuda_getDevice() == dev:
-        if stream is None:
-            stream = c._cuda_getCurrentRawStream(dev)
-        st = fn(*args, getattr(stream, "cuda_stream", stream))
+        st = fn(*args, stream)
     else:
-        with _torch().cuda.device(dev):
-            if stream is None:
-                stream = c._cuda_getCurrentRawStream(dev)
-            st = fn(*args, getattr(stream, "cuda_stream", stream))
+        with _torch_module.cuda.device(dev):
+            st = fn(*args, stream)
     if st != 0:
         raise JetLongError(st, where)
 
@@ -568,20 +563,23 @@ def jl_qk_norm_rope(q, k, q_weight, k_weight, positions, q_out, k_out, *, eps: f
     k [T, Hkv, D] (bf16, CUDA; views of a fused projection are fine), weights [D] bf16 or None
     (no norm on that side), positions int32 [T] (-1: padded token, left alone), q_out / k_out
     contiguous (they may be q / k)."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     dev = _device_of(q, "q")
-    qs, ks = _head_rows(q, "q", T, Hq, D, dev), _head_rows(k, "k", T, Hkv, D, dev)
     bf16, i32 = torch.bfloat16, torch.int32
+    qs, ks = _head_rows(dev, bf16, q, "q", T, Hq, D), _head_rows(dev, bf16, k, "k", T, Hkv, D)
     _check_on(dev, ((positions, "positions", i32, (T,)), (q_out, "q_out", bf16, (T, Hq, D)),
                     (k_out, "k_out", bf16, (T, Hkv, D))))
-    _check_opt(dev, q_weight, "q_weight", bf16, (D,))
-    _check_opt(dev, k_weight, "k_weight", bf16, (D,))
-    _check_error_word(dev, dev_error)
-    _call(dev, lib().jl_qk_norm_rope, "jl_qk_norm_rope", q.data_ptr(), qs, k.data_ptr(), ks, _addr(q_weight), _addr(k_weight),
-          float(eps), positions.data_ptr(), q_out.data_ptr(), _addr(k_out), T, Hq, Hkv, D, float(rope_base), _addr(dev_error),
-          stream=stream)
+    if q_weight is not None:
+        _check_on(dev, ((q_weight, "q_weight", bf16, (D,)),))
+    if k_weight is not None:
+        _check_on(dev, ((k_weight, "k_weight", bf16, (D,)),))
+    if dev_error is not None:
+        _check_on(dev, ((dev_error, "dev_error", i32, dev_error.shape),))
+    _call(dev, lib().jl_qk_norm_rope, "jl_qk_norm_rope", q.data_ptr(), qs, k.data_ptr(), ks, _addr(q_weight),
+          _addr(k_weight), float(eps), positions.data_ptr(), q_out.data_ptr(), _addr(k_out), T, Hq, Hkv, D,
+          float(rope_base), _addr(dev_error), stream=stream)
 
 
 def jl_qk_norm_rope_append_paged(q, k, v, q_weight, k_weight, seq_ids, positions, block_table, q_out, k_pages,
@@ -589,25 +587,31 @@ def jl_qk_norm_rope_append_paged(q, k, v, q_weight, k_weight, seq_ids, positions
     """jl_qk_norm_rope whose keys, and the values v [T, Hkv, D], go to row positions[t] of
     sequence seq_ids[t] (int32 [T], a row of block_table int32 [B, max_pages]) of the paged
     cache; k_out [T, Hkv, D] (or None) receives the keys too."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     dev = _device_of(q, "q")
-    qs, ks = _head_rows(q, "q", T, Hq, D, dev), _head_rows(k, "k", T, Hkv, D, dev)
-    vs = _head_rows(v, "v", T, Hkv, D, dev)
     bf16, i32 = torch.bfloat16, torch.int32
+    qs, ks = _head_rows(dev, bf16, q, "q", T, Hq, D), _head_rows(dev, bf16, k, "k", T, Hkv, D)
+    vs = _head_rows(dev, bf16, v, "v", T, Hkv, D)
     B, M = block_table.shape
     _check_on(dev, ((seq_ids, "seq_ids", i32, (T,)), (positions, "positions", i32, (T,)),
                     (block_table, "block_table", i32, (B, M)), (q_out, "q_out", bf16, (T, Hq, D))))
-    _check_opt(dev, k_out, "k_out", bf16, (T, Hkv, D))
-    _check_opt(dev, q_weight, "q_weight", bf16, (D,))
-    _check_opt(dev, k_weight, "k_weight", bf16, (D,))
-    _check_error_word(dev, dev_error)
-    kv = _paged_kv(k_pages, v_pages, dev, Hkv, D)
-    _call(dev, lib().jl_qk_norm_rope_append_paged, "jl_qk_norm_rope_append_paged", q.data_ptr(), qs, k.data_ptr(), ks,
-          v.data_ptr(), vs, _addr(q_weight), _addr(k_weight), float(eps), seq_ids.data_ptr(), positions.data_ptr(), q_out.data_ptr(),
-          _addr(k_out), ctypes.byref(kv), block_table.data_ptr(), M, T, B, Hq, Hkv, D, float(rope_base), _addr(dev_error),
-          stream=stream)
+    if k_out is not None:
+        _check_on(dev, ((k_out, "k_out", bf16, (T, Hkv, D)),))
+    if q_weight is not None:
+        _check_on(dev, ((q_weight, "q_weight", bf16, (D,)),))
+    if k_weight is not None:
+        _check_on(dev, ((k_weight, "k_weight", bf16, (D,)),))
+    if dev_error is not None:
+        _check_on(dev, ((dev_error, "dev_error", i32, dev_error.shape),))
+    kv = _paged_kv(dev, bf16, k_pages, v_pages, D)
+    if k_pages.shape[2] != Hkv:
+        raise ValueError(f"k_pages holds {k_pages.shape[2]} heads, expected {Hkv}")
+    _call(dev, lib().jl_qk_norm_rope_append_paged, "jl_qk_norm_rope_append_paged", q.data_ptr(), qs,
+          k.data_ptr(), ks, v.data_ptr(), vs, _addr(q_weight), _addr(k_weight), float(eps), seq_ids.data_ptr(),
+          positions.data_ptr(), q_out.data_ptr(), _addr(k_out), ctypes.byref(kv), block_table.data_ptr(), M, T,
+          B, Hq, Hkv, D, float(rope_base), _addr(dev_error), stream=stream)
 
 
 def jl_decode_paged_workspace_bytes(Hq: int, Hkv: int, head_dim: int) -> int:
@@ -615,18 +619,18 @@ def jl_decode_paged_workspace_bytes(Hq: int, Hkv: int, head_dim: int) -> int:
 
 
 def _decode_paged_tensors(q, k_pages, v_pages, block_table, seq_lens, o, lse, workspace, dev_error):
-    torch = _torch()
+    torch = _torch_module or _torch()
     B, Hq, D = q.shape
     dev = _device_of(q, "q")
     bf16, i32 = torch.bfloat16, torch.int32
     M = block_table.shape[1]
     _check_on(dev, ((q, "q", bf16, (B, Hq, D)), (block_table, "block_table", i32, (B, M)),
                     (seq_lens, "seq_lens", i32, (B,)), (o, "o", bf16, (B, Hq, D))))
-    _check_opt(dev, lse, "lse", torch.float32, (B, Hq))
-    _check_error_word(dev, dev_error)
-    kv = _paged_kv(k_pages, v_pages, dev)
-    if k_pages.shape[3] != D:
-        raise ValueError(f"k_pages holds rows of {k_pages.shape[3]}, expected {D}")
+    if lse is not None:
+        _check_on(dev, ((lse, "lse", torch.float32, (B, Hq)),))
+    if dev_error is not None:
+        _check_on(dev, ((dev_error, "dev_error", i32, dev_error.shape),))
+    kv = _paged_kv(dev, bf16, k_pages, v_pages, D)
     return B, Hq, k_pages.shape[2], D, M, dev, kv, _workspace(dev, workspace)
 
 
@@ -639,9 +643,9 @@ def jl_bifocal_decode_paged(q, k_pages, v_pages, block_table, seq_lens, o, lse, 
     B, Hq, Hkv, D, M, dev, kv, ws_bytes = _decode_paged_tensors(q, k_pages, v_pages, block_table, seq_lens, o, lse,
                                                                 workspace, dev_error)
     _call(dev, lib().jl_bifocal_decode_paged, "jl_bifocal_decode_paged", q.data_ptr(), ctypes.byref(kv),
-          block_table.data_ptr(), M, seq_lens.data_ptr(), o.data_ptr(), _addr(lse), B, Hq, Hkv, D, int(w0), int(w_pretrained),
-          float(rope_base), float(softmax_scale), int(mode), _addr(workspace), ws_bytes, _addr(dev_error),
-          stream=stream)
+          block_table.data_ptr(), M, seq_lens.data_ptr(), o.data_ptr(), _addr(lse), B, Hq, Hkv, D, int(w0),
+          int(w_pretrained), float(rope_base), float(softmax_scale), int(mode), _addr(workspace), ws_bytes,
+          _addr(dev_error), stream=stream)
 
 
 def jl_bifocal_decode_paged_sparse(q, k_pages, v_pages, block_table, seq_lens, page_list, page_counts, o, lse, *,
@@ -649,16 +653,17 @@ def jl_bifocal_decode_paged_sparse(q, k_pages, v_pages, block_table, seq_lens, p
                                    mode: int = JL_QSHIFT_SELF_EXTEND, workspace=None, dev_error=None, stream=None):
     """jl_bifocal_decode_paged over the pages that page_list int32 [B, Hkv, n] names (logical
     pages, the first page_counts[b, g] of each row; page_counts int32 [B, Hkv])."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     B, Hq, Hkv, D, M, dev, kv, ws_bytes = _decode_paged_tensors(q, k_pages, v_pages, block_table, seq_lens, o, lse,
                                                                 workspace, dev_error)
     n = page_list.shape[2]
     _check_on(dev, ((page_list, "page_list", torch.int32, (B, Hkv, n)),
                     (page_counts, "page_counts", torch.int32, (B, Hkv))))
-    _call(dev, lib().jl_bifocal_decode_paged_sparse, "jl_bifocal_decode_paged_sparse", q.data_ptr(), ctypes.byref(kv),
-          block_table.data_ptr(), M, seq_lens.data_ptr(), page_list.data_ptr(), n, page_counts.data_ptr(), o.data_ptr(), _addr(lse), B,
-          Hq, Hkv, D, int(w0), int(w_pretrained), float(rope_base), float(softmax_scale), int(mode), _addr(workspace),
-          ws_bytes, _addr(dev_error), stream=stream)
+    _call(dev, lib().jl_bifocal_decode_paged_sparse, "jl_bifocal_decode_paged_sparse", q.data_ptr(),
+          ctypes.byref(kv), block_table.data_ptr(), M, seq_lens.data_ptr(), page_list.data_ptr(), n,
+          page_counts.data_ptr(), o.data_ptr(), _addr(lse), B, Hq, Hkv, D, int(w0), int(w_pretrained),
+          float(rope_base), float(softmax_scale), int(mode), _addr(workspace), ws_bytes, _addr(dev_error),
+          stream=stream)
 
 
 def jl_page_summaries(k_pages, block_table, starts, seq_lens, summaries, *, max_new: int, rope_base: float,
@@ -666,18 +671,19 @@ def jl_page_summaries(k_pages, block_table, starts, seq_lens, summaries, *, max_
     """Mean key of every page that holds positions starts[b] .. seq_lens[b] - 1 (int32 [B]) into
     summaries [num_pages, Hkv, D] (bf16, contiguous, indexed like the pages); max_new >= every
     seq_lens[b] - starts[b]."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     B, M = block_table.shape
     dev = _device_of(k_pages, "k_pages")
     n, _, Hkv, D = k_pages.shape
     i32 = torch.int32
     _check_on(dev, ((block_table, "block_table", i32, (B, M)), (starts, "starts", i32, (B,)),
                     (seq_lens, "seq_lens", i32, (B,)), (summaries, "summaries", torch.bfloat16, (n, Hkv, D))))
-    _check_error_word(dev, dev_error)
-    kv = _paged_kv(k_pages, None, dev)
-    _call(dev, lib().jl_page_summaries, "jl_page_summaries", ctypes.byref(kv), block_table.data_ptr(), M, starts.data_ptr(),
-          seq_lens.data_ptr(), int(max_new), summaries.data_ptr(), B, Hkv, D, float(rope_base), _addr(dev_error),
-          stream=stream)
+    if dev_error is not None:
+        _check_on(dev, ((dev_error, "dev_error", i32, dev_error.shape),))
+    kv = _paged_kv(dev, torch.bfloat16, k_pages, None)
+    _call(dev, lib().jl_page_summaries, "jl_page_summaries", ctypes.byref(kv), block_table.data_ptr(), M,
+          starts.data_ptr(), seq_lens.data_ptr(), int(max_new), summaries.data_ptr(), B, Hkv, D,
+          float(rope_base), _addr(dev_error), stream=stream)
 
 
 def jl_select_pages_workspace_bytes(B: int, Hkv: int, max_pages: int) -> int:
@@ -691,7 +697,7 @@ def jl_select_pages(q, summaries, block_table, seq_lens, page_list, page_counts,
     best by score, per KV head, ascending into page_list int32 [B, Hkv, n] (-1 behind them) and
     page_counts int32 [B, Hkv].  n >= min(max_pages, sink_pages + top_k + ceil(w0 / page_size) + 1);
     workspace: uint8 CUDA tensor of jl_select_pages_workspace_bytes(...) bytes."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     B, Hq, D = q.shape
     num_pages, Hkv, _ = summaries.shape
     M = block_table.shape[1]
@@ -701,9 +707,10 @@ def jl_select_pages(q, summaries, block_table, seq_lens, page_list, page_counts,
     _check_on(dev, ((q, "q", bf16, (B, Hq, D)), (summaries, "summaries", bf16, (num_pages, Hkv, D)),
                     (block_table, "block_table", i32, (B, M)), (seq_lens, "seq_lens", i32, (B,)),
                     (page_list, "page_list", i32, (B, Hkv, n)), (page_counts, "page_counts", i32, (B, Hkv))))
-    _check_error_word(dev, dev_error)
+    if dev_error is not None:
+        _check_on(dev, ((dev_error, "dev_error", i32, dev_error.shape),))
     ws_bytes = _workspace(dev, workspace)
-    _call(dev, lib().jl_select_pages, "jl_select_pages", q.data_ptr(), summaries.data_ptr(), num_pages, int(page_size),
-          block_table.data_ptr(), M, seq_lens.data_ptr(), int(sink_pages), int(top_k), page_list.data_ptr(), n,
-          page_counts.data_ptr(), B, Hq, Hkv, D, int(w0), int(w_pretrained), float(rope_base), int(mode),
-          _addr(workspace), ws_bytes, _addr(dev_error), stream=stream)
+    _call(dev, lib().jl_select_pages, "jl_select_pages", q.data_ptr(), summaries.data_ptr(), num_pages,
+          int(page_size), block_table.data_ptr(), M, seq_lens.data_ptr(), int(sink_pages), int(top_k),
+          page_list.data_ptr(), n, page_counts.data_ptr(), B, Hq, Hkv, D, int(w0), int(w_pretrained),
+          float(rope_base), int(mode), _addr(workspace), ws_bytes, _addr(dev_error), stream=stream)
