@@ -84,6 +84,12 @@ struct PgCfg {
   static_assert(kSmem <= 232448, "shared memory");
 };
 
+// a / b of non-negative numbers; 64-bit divisions only where they are needed (a fifth of
+// a microsecond each).
+__device__ __forceinline__ int64_t div_units(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Units of item it = b * Hkv + g.
 __device__ __forceinline__ int item_units(const PagedDecodeArgs& a, int it) {
   const int b = it / a.Hkv;
@@ -270,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t want = (U + kMinUnits - 1) / kMinUnits;
     N = want < gridDim.x ? want : gridDim.x;
     if (blockIdx.x >= N) return;
-    c0 = (int64_t)blockIdx.x * U / N;
-    c1 = ((int64_t)blockIdx.x + 1) * U / N;
+    c0 = div_units((int64_t)blockIdx.x * U, N);
+    c1 = div_units(((int64_t)blockIdx.x + 1) * U, N);
     wb = c0 + warp * (c1 - c0) / kWarps;
     we = c0 + (warp + 1) * (c1 - c0) / kWarps;
   } else {
@@ -847,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* wts = reinterpret_cast<float*>(smem + C::kWtsOff);  // [r][kMaxParts]
   float* part_l = wts + kMaxR * C::kMaxParts;                 // [r][kMaxParts] the parts' sums
   float* tot = part_l + kMaxR * C::kMaxParts;                 // [r] maxima, then [r] sums
-  auto cta_of = [&](int64_t unit) -> int { return (int)(((unit + 1) * N - 1) / U); };
+  auto cta_of = [&](int64_t unit) -> int { return (int)div_units((unit + 1) * N - 1, U); };
   __threadfence();
   __syncthreads();
   if (tid < 2 && (tid == 0 ? shared_item[0] : shared_item[1]) >= 0) {
@@ -930,11 +936,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool kPack>
 cudaError_t launch_dp(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedDecodeArgs& a,
                       cudaStream_t stream) {
+  // The shared-memory attribute is set once per device (1 us, a third of a short call's
+  // host side) and again where a launch is refused for it, as after cudaDeviceReset.
+  static std::atomic<uint64_t> set{0};
   auto k = paged_decode_kernel<D, kPack>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PgCfg<D>::kSmem);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  k<<<decode_paged_max_ctas(), kThreads, PgCfg<D>::kSmem, stream>>>(tm_k, tm_v, a);  // one CTA per SM
-  return cudaGetLastError();
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  for (bool known = (set.load(std::memory_order_relaxed) & bit) != 0;; known = false) {
+    if (!known) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PgCfg<D>::kSmem);
+      if (e != cudaSuccess) return e;
+      set.fetch_or(bit, std::memory_order_relaxed);
+    }
+    k<<<decode_paged_max_ctas(), kThreads, PgCfg<D>::kSmem, stream>>>(tm_k, tm_v, a);  // one CTA per SM
+    e = cudaGetLastError();
+    if (e != cudaErrorInvalidValue || !known) return e;
+  }
 }
 
 }  // namespace
