@@ -23,7 +23,7 @@ namespace jl {
 namespace {
 
 constexpr int kSumThreads = 256;
-constexpr int kSumBlocksPerSm = 3;  // resident at 80 registers a thread
+constexpr int kSumBlocksPerSm = 2;  // resident (three spill: 54 against 52 us for 2048 pages of 64 keys, 8 heads)
 constexpr int kScoreThreads = 256;
 constexpr int kMaxTile = 128;       // pages per CTA of the score kernel, at most
 constexpr int kHeadBlock = 8;       // KV heads whose turned queries a CTA of the score kernel holds
@@ -61,43 +61,66 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm)
   constexpr int kLanes = D / 16;
   constexpr int kStep = 32 / kLanes;  // rows per pass
   constexpr int kAhead = 4;
+  __shared__ __align__(16) float4 turn_in[kStep][H2 / 2];  // R(m - grp): (c, c, s, s) of two pairs
   const int lane = threadIdx.x & 31;
   const int sub = lane % kLanes, grp = lane / kLanes;
   const int P = a.pages.page_size;
-  float sc[8], ss[8], mc[8], ms[8];  // R(-step), R(m - grp)
+  float sc[8], ss[8];  // R(-step)
   {
     const uint64_t* tp = a.turn;  // a generic read: an indexed parameter read serialises
     asm volatile("" : "+l"(tp));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint64_t turn = tp[8 * sub + e];
-      sincos_fixed(-kStep, turn, &ss[e], &sc[e]);
-      sincos_fixed(P / 2 - grp, turn, &ms[e], &mc[e]);
+    for (int e = 0; e < 8; ++e) sincos_fixed(-kStep, tp[8 * sub + e], &ss[e], &sc[e]);
+    for (int i = threadIdx.x; i < kStep * (H2 / 2); i += kSumThreads) {
+      const int row = i / (H2 / 2), t = i % (H2 / 2);
+      float4 f;
+      sincos_fixed(P / 2 - row, tp[2 * t], &f.z, &f.x);
+      sincos_fixed(P / 2 - row, tp[2 * t + 1], &f.w, &f.y);
+      turn_in[row][t] = f;
     }
+    __syncthreads();
   }
   const int64_t tasks = (int64_t)a.B * a.pages_per_seq * a.Hkv;
   const int64_t nwarps = (int64_t)gridDim.x * (kSumThreads / 32);
-  for (int64_t task = ((int64_t)blockIdx.x * kSumThreads + threadIdx.x) >> 5; task < tasks; task += nwarps) {
-    const int64_t bp = task / a.Hkv;
-    const int g = (int)(task - bp * a.Hkv);
-    const int b = (int)(bp / a.pages_per_seq);
-    const int i = (int)(bp - (int64_t)b * a.pages_per_seq);
-    const int L = a.seq_lens[b], start = a.starts[b];
-    const bool ok = paged_length_ok(L, a.max_pages, P) && start >= 0;
-    // more new pages than the call was sized for: refuse the sequence
-    const bool over = ok && start < L && (L - 1) / P - start / P >= a.pages_per_seq;
-    if (!ok || over) {
-      if (lane == 0 && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
-      continue;
+  int64_t task = ((int64_t)blockIdx.x * kSumThreads + threadIdx.x) >> 5;
+  // A task's page in the pool, its keys and its head; described one task ahead.
+  int next_phys = -1, next_n = 0, next_g = 0;
+  auto describe = [&](int64_t t) {
+    next_n = 0;
+    if (t >= tasks) return;
+    int b, i;
+    if (tasks <= 0xffffffffll) {
+      const unsigned bp = (unsigned)t / (unsigned)a.Hkv;
+      next_g = (int)((unsigned)t - bp * a.Hkv);
+      b = (int)(bp / (unsigned)a.pages_per_seq);
+      i = (int)(bp - (unsigned)b * a.pages_per_seq);
+    } else {
+      const int64_t bp = t / a.Hkv;
+      next_g = (int)(t - bp * a.Hkv);
+      b = (int)(bp / a.pages_per_seq);
+      i = (int)(bp - (int64_t)b * a.pages_per_seq);
     }
-    const int lp = start / P + i;
-    if (start >= L || lp > (L - 1) / P) continue;
-    const int phys = a.block_table[(int64_t)b * a.max_pages + lp];
+    const int L = a.seq_lens[b], start = a.starts[b];
+    bool ok = paged_length_ok(L, a.max_pages, P) && start >= 0;
+    const int first = start / P, lp = first + i;
+    // more new pages than the call was sized for: refuse the sequence
+    ok = ok && !(start < L && (L - 1) / P - first >= a.pages_per_seq);
+    if (!ok) {
+      if (lane == 0 && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
+    } else if (start < L && lp <= (L - 1) / P) {
+      next_n = min(P, L - lp * P);
+      next_phys = a.block_table[(int64_t)b * a.max_pages + lp];
+    }
+  };
+  describe(task);
+  for (; task < tasks; task += nwarps) {
+    const int n = next_n, phys = next_phys, g = next_g;
+    describe(task + nwarps);
+    if (n == 0) continue;
     if (phys < 0 || phys >= a.pages.num_pages) {
       if (lane == 0 && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
       continue;
     }
-    const int n = min(P, L - lp * P);
     const __nv_bfloat16* base =
         a.pages.k + phys * a.pages.page_stride + g * a.pages.head_stride + grp * a.pages.row_stride + 8 * sub;
     float x[8], y[8];
@@ -131,8 +154,10 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm)
     const float inv = 1.f / (float)n;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float xr = x[e] * mc[e] - y[e] * ms[e];
-      y[e] = y[e] * mc[e] + x[e] * ms[e];
+      const float4 f = turn_in[grp][4 * sub + e / 2];
+      const float c = (e & 1) ? f.y : f.x, sn = (e & 1) ? f.w : f.z;
+      const float xr = x[e] * c - y[e] * sn;
+      y[e] = y[e] * c + x[e] * sn;
       x[e] = xr;
 #pragma unroll
       for (int m = kLanes; m < 32; m <<= 1) {
@@ -237,6 +262,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const __gr
   const int L = a.seq_lens[b];
   const int G = (int)group_size(L, a.w_pretrained);
   const int dq = (int)(query_remote(L - 1, G, query_shift(a.w0, G, a.qshift)) - (L - 1));
+  const unsigned g_inv = 0xffffffffu / (unsigned)G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c4 = lane & 3, hrow = lane >> 2;
   // the two pairs whose factors this lane forms: place (j, i, c4) of a row is pairs 8 (c4 + 4 j) + 2 i, + 1
@@ -320,9 +346,13 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const __gr
       load(g0);
       __syncwarp();
       {
-        int c = page0 * P + P / 2;
+        unsigned c = page0 * P + P / 2;
 #pragma unroll 4
-        for (int u = 0; u < 16; ++u, c += P) table[u * kRow + fl] = factors(c / G - c);
+        for (int u = 0; u < 16; ++u, c += P) {
+          unsigned qd = __umulhi(c, g_inv);  // c / G or one less
+          if (c - qd * G >= (unsigned)G) ++qd;
+          table[u * kRow + fl] = factors((int)(qd - c));
+        }
       }
       __syncwarp();
       const float4* er[2] = {table + hrow * kRow + c4, table + (hrow + 8) * kRow + c4};
