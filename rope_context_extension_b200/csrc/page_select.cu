@@ -25,7 +25,7 @@ namespace {
 constexpr int kSumThreads = 256;
 constexpr int kSumBlocksPerSm = 2;  // resident (three spill: 54 against 52 us for 2048 pages of 64 keys, 8 heads)
 constexpr int kScoreThreads = 256;
-constexpr int kMaxTile = 128;       // pages per CTA of the score kernel, at most
+constexpr int kMaxTile = 256;       // pages per CTA of the score kernel, at most
 constexpr int kHeadBlock = 8;       // KV heads whose turned queries a CTA of the score kernel holds
 constexpr int kSelThreads = 512;
 constexpr int kRank = 128;          // pages between the edges that are ranked by comparing all
@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const __gr
   constexpr int kWarps = kScoreThreads / 32;
   constexpr int kRow = ScoreSmem<D>::kRow;
   extern __shared__ __align__(16) uint8_t score_smem[];
+  asm volatile("griddepcontrol.launch_dependents;");  // the selection may take its place; it waits for the scores
   ScoreSmem<D>& sm = *reinterpret_cast<ScoreSmem<D>*>(score_smem);
   const int b = blockIdx.y;
   const PageSpan sp = page_span(a, b);
@@ -457,13 +458,15 @@ template <int D>
 __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_constant__ PageSelectArgs a) {
   constexpr int kWarps = kSelThreads / 32;
   constexpr int kPer = 8;          // pages of a thread per step of an ordered pass
-  __shared__ int hist[256];        // this CTA's counts, read by the cluster
-  __shared__ int share[2];         // this CTA's running counts, read by the cluster
+  __shared__ int hist[4][256];     // this CTA's counts of each pass, read by the cluster
+  __shared__ int total_hist[256];  // the cluster's
+  __shared__ int share[4];         // this CTA's running counts, read by the cluster
   __shared__ int wcount[kWarps];
   __shared__ int found[3];         // bucket, keys above it, keys in it
   __shared__ uint32_t rkey[kRank];
   __shared__ float wmax[kWarps];
   const int CL = gridDim.x, rank = blockIdx.x;  // the cluster is the grid's x
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // all that was launched before is done
   const int g = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = (int64_t)b * a.Hkv + g;
@@ -484,29 +487,28 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
     int shift = 32, in_bucket = 0;
     do {
       shift -= 8;
-      if (tid < 256) hist[tid] = 0;
+      int* h = hist[shift / 8];
+      if (tid < 256) h[tid] = 0;
       __syncthreads();
       for (int p = begin + tid; p < end; p += kSelThreads) {
         const uint32_t key = key_at(p);
-        if (shift == 24 || (key >> (shift + 8)) == (thr >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255u], 1);
+        if (shift == 24 || (key >> (shift + 8)) == (thr >> (shift + 8))) atomicAdd(&h[(key >> shift) & 255u], 1);
+      }
+      if (CL > 1)
+        cluster_sync();
+      else
+        __syncthreads();
+      if (tid < 256) {
+        int sum = h[tid];
+        for (int k = 1; k < CL; ++k) sum += cluster_ld(&h[tid], (rank + k) % CL);
+        total_hist[tid] = sum;
       }
       __syncthreads();
-      if (CL > 1) {
-        cluster_sync();
-        int sum = 0;
-        if (tid < 256) {
-          sum = hist[tid];
-          for (int k = 1; k < CL; ++k) sum += cluster_ld(&hist[tid], (rank + k) % CL);
-        }
-        cluster_sync();  // every CTA has read the others' counts
-        if (tid < 256) hist[tid] = sum;
-        __syncthreads();
-      }
       if (warp == 0) {  // the bucket, from the top, that holds the need-th key
         int c[8], sum = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          c[i] = hist[255 - (8 * lane + i)];
+          c[i] = total_hist[255 - (8 * lane + i)];
           sum += c[i];
         }
         int incl = sum;
@@ -536,21 +538,31 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
     } while (shift > 0 && (shift > 16 || in_bucket > few));
     return shift;
   };
-  // Sum of v over the CTAs before this one, and over all; v is the same for every thread.
-  auto before = [&](int v, int which, int& all) {
-    all = v;
-    if (CL == 1) return 0;
-    if (tid == 0) share[which] = v;
-    cluster_sync();
-    int sum = 0;
-    for (int k = 0; k < CL; ++k) {
-      if (k == rank) continue;
-      const int t = cluster_ld(&share[which], k);
-      all += t;
-      if (k < rank) sum += t;
+  // Sums of v and w over the CTAs before this one, and over all; v, w are the same for
+  // every thread of a CTA.  Each call has its own two slots of `share`.
+  auto before = [&](int slot, int& v, int& w, int& v_all, int& w_all) {
+    v_all = v;
+    w_all = w;
+    int vs = 0, ws = 0;
+    if (CL > 1) {
+      if (tid == 0) {
+        share[slot] = v;
+        share[slot + 1] = w;
+      }
+      cluster_sync();
+      for (int k = 0; k < CL; ++k) {
+        if (k == rank) continue;
+        const int vk = cluster_ld(&share[slot], k), wk = cluster_ld(&share[slot + 1], k);
+        v_all += vk;
+        w_all += wk;
+        if (k < rank) {
+          vs += vk;
+          ws += wk;
+        }
+      }
     }
-    cluster_sync();
-    return sum;
+    v = vs;
+    w = ws;
   };
   // Sum of v over the CTA's threads before this one, and over all of them.
   auto scan_of = [&](int v, int& total) {
@@ -620,9 +632,8 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
       scan_of(__popc(up), n);
       kept += n;
     }
-    int kept_all, amb_all;
-    before(kept, 0, kept_all);
-    const int amb_first = before(amb, 1, amb_all);
+    int kept_first = kept, amb_first = amb, kept_all, amb_all;
+    before(0, kept_first, amb_first, kept_all, amb_all);
     need = a.top_k - kept_all;
     __syncthreads();
     if (need == amb_all) {  // every one of them is kept
@@ -684,13 +695,15 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
         }
         kept += __syncthreads_count(keep);
       } else {
+        if (CL > 1) cluster_sync();  // the first search's counts have been read
         select([&](int i) { return score_key(amb_score[i]); }, 0, amb, need, 0);
         // larger keys are kept, and of the equal ones the first `need` in page order
         int ties = 0;
         for (int i = tid; i < amb; i += kSelThreads) ties += score_key(amb_score[i]) == thr;
         int n, tie_all;
         scan_of(ties, n);
-        int seen = before(n, 0, tie_all);
+        int seen = n, none = 0, none_all;
+        before(2, seen, none, tie_all, none_all);
         for (int base = 0; base < amb; base += kSelThreads) {
           const int i = base + tid;
           const uint32_t key = i < amb ? score_key(amb_score[i]) : 0u;
@@ -709,9 +722,21 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
 
   // The kept pages, in page order, behind those of the CTAs before.
   const int open = all ? max(0, send - sbegin) : kept;
-  const int mine = max(0, min(end, sp.sink) - begin) + open + max(0, end - max(begin, sp.band));
-  int total;
-  int written = before(mine, 0, total), run = 0;
+  const int total = sp.pages == 0 ? 0 : sp.sink + min(cand, a.top_k) + sp.pages - sp.band;
+  int written = max(0, min(end, sp.sink) - begin) + open + max(0, end - max(begin, sp.band)), run = 0;
+  if (CL > 1) {
+    // (the slots' earlier counts have been read: every use of them ends at a barrier of
+    // the cluster before this one, or does here)
+    cluster_sync();
+    if (tid == 0) share[0] = written;
+    cluster_sync();
+    int sum = 0;
+    for (int k = 0; k < rank; ++k) sum += cluster_ld(&share[0], k);
+    written = sum;
+    cluster_sync();  // no CTA leaves while another reads its counts
+  } else {
+    written = 0;
+  }
   for (int base = begin; base < end; base += kPer * kSelThreads) {
     const int p0 = base + kPer * tid;
     unsigned keep = 0, in = 0;
@@ -780,12 +805,12 @@ cudaError_t launch_score(const PageSelectArgs& a, dim3 grid, cudaStream_t stream
 cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream) {
   cudaError_t e;
   if (a.top_k > 0) {
-    // Tiles of up to 128 pages share a factor table; smaller ones while the tiles do
-    // not fill the GPU (two CTAs per SM).
+    // One round of CTAs (two per SM) where tiles of up to kMaxTile pages give it: with
+    // 1.7 rounds 2048 pages of eight sequences took 17 us instead of 11.
     const int sms = current_device_sms();
     if (sms == 0) return cudaErrorNoDevice;
-    a.tile_pages = kMaxTile;
-    while (a.tile_pages > 16 && (a.max_pages + a.tile_pages - 1) / a.tile_pages * a.B < 2 * sms) a.tile_pages /= 2;
+    const int64_t each = (a.max_pages * a.B + 2 * sms - 1) / (2 * sms);
+    a.tile_pages = (int)std::min<int64_t>(kMaxTile, (each + 15) / 16 * 16);
     const dim3 grid((unsigned)((a.max_pages + a.tile_pages - 1) / a.tile_pages), a.B);
     if ((e = D == 128 ? launch_score<128>(a, grid, stream) : launch_score<64>(a, grid, stream)) != cudaSuccess) return e;
   }
@@ -796,13 +821,15 @@ cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream) {
   cfg.gridDim = dim3(cl, a.Hkv, a.B);
   cfg.blockDim = dim3(kSelThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cl;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   const PageSelectArgs& ca = a;
   return D == 128 ? cudaLaunchKernelEx(&cfg, page_select_kernel<128>, ca)
                   : cudaLaunchKernelEx(&cfg, page_select_kernel<64>, ca);
