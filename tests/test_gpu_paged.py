@@ -128,6 +128,21 @@ def test_norm_rope(T, Hq, Hkv, D, norm):
         assert np.all(_f64(out)[~live] == 7.0)
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(9001, 3, 1, 64), (5000, 40, 8, 128)])
+def test_norm_rope_many_tokens(T, Hq, Hkv, D):
+    g = torch.Generator().manual_seed(T)
+    q, k = _randn(g, T, Hq, D), _randn(g, T, Hkv, D)
+    w = _randn(g, D)
+    pos = torch.arange(T)
+    pos[::7] = -1
+    qo, ko = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    jl.jl_qk_norm_rope(q, k, w, None, pos.to(torch.int32).to(DEV), qo, ko, eps=ph.EPS, rope_base=1e6)
+    for src, ww, out in ((q, w, qo), (k, None, ko)):
+        want = ph.norm_rope(_f64(src), None if ww is None else _f64(ww), pos.numpy(), 1e6)
+        want[::7] = 7.0
+        assert np.all(np.abs(_f64(out) - want) <= ph.norm_rope_tol(want))
+
+
 def test_norm_rope_of_zero_rows_and_in_place():
     g = torch.Generator().manual_seed(2)
     q, k = _randn(g, 5, 4, 128), _randn(g, 5, 2, 128)
@@ -248,6 +263,56 @@ def test_decode_with_outlier_keys_and_one_dominant_key():
     jl.jl_bifocal_decode_paged(q, k, v, table, _i32(lens), o, lse, w0=100, w_pretrained=1000, rope_base=1e6,
                                workspace=_ws(Hq, Hkv, D))
     _check_decode(o, lse, q, k, v, table, lens, 100, 1000, 1e6)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D,top,P", [(300, 4, 2, 64, 60, 16), (300, 2, 2, 128, 400, 32), (40, 24, 3, 64, 130, 16),
+                                              (700, 1, 1, 64, 17, 16), (97, 32, 8, 128, 300, 48)])
+def test_decode_many_short_sequences(B, Hq, Hkv, D, top, P):
+    # more items than the work line's runs; sequences that warps take whole, and a mix
+    g = torch.Generator().manual_seed(B + top)
+    lens = torch.randint(0, top + 1, (B,), generator=g).tolist()
+    lens[0], lens[-1] = top, 0
+    n = sum(-(-x // P) for x in lens) + 1
+    k, v = _pool(g, n, P, Hkv, D)
+    table = _table(g, lens, P, n)
+    _stale(k, v, table, lens, float("inf"))
+    q = _randn(g, B, Hq, D)
+    o, lse = torch.full_like(q, 7.0), torch.full((B, Hq), 7.0, device=DEV)
+    err, ws = _i32([0]), _ws(Hq, Hkv, D)
+    jl.jl_bifocal_decode_paged(q, k, v, table, _i32(lens), o, lse, w0=9, w_pretrained=30, rope_base=1e4, workspace=ws,
+                               dev_error=err)
+    assert int(err) == 0
+    _check_decode(o, lse, q, k, v, table, lens, 9, 30, 1e4)
+    assert torch.all(ws[:4 * 148] == 0)  # the tickets are back at zero
+
+
+@pytest.mark.parametrize("W", [1, 2, 37, 1500, 2999])
+def test_decode_group_sizes(W):
+    # G = 3000, 1500, 82, 2, 2: how far the keys' turns carry from one unit to the next
+    g = torch.Generator().manual_seed(W)
+    lens, P, Hq, Hkv, D = [3000, 2999], 32, 4, 1, 128
+    k, v = _pool(g, 200, P, Hkv, D)
+    table = _table(g, lens, P, 200)
+    q = _randn(g, 2, Hq, D)
+    o, lse = torch.empty_like(q), torch.empty(2, Hq, device=DEV)
+    jl.jl_bifocal_decode_paged(q, k, v, table, _i32(lens), o, lse, w0=33, w_pretrained=W, rope_base=1e6,
+                               workspace=_ws(Hq, Hkv, D))
+    _check_decode(o, lse, q, k, v, table, lens, 33, W, 1e6)
+
+
+@pytest.mark.parametrize("at", [5, 990])  # a remote key, a local one
+def test_a_nan_key_reaches_its_own_head_only(at):
+    g = torch.Generator().manual_seed(at)
+    lens, P, Hq, Hkv, D = [1000, 1000], 16, 8, 2, 128
+    k, v = _pool(g, 130, P, Hkv, D)
+    table = _table(g, lens, P, 130)
+    k[int(table[0, at // P]), at % P, 1, 7] = float("nan")
+    q = _randn(g, 2, Hq, D)
+    o, lse = torch.empty_like(q), torch.empty(2, Hq, device=DEV)
+    jl.jl_bifocal_decode_paged(q, k, v, table, _i32(lens), o, lse, w0=100, w_pretrained=300, rope_base=1e6,
+                               workspace=_ws(Hq, Hkv, D))
+    assert torch.isnan(o[0, 4:]).all() and torch.isnan(lse[0, 4:]).all()
+    assert torch.isfinite(o[0, :4]).all() and torch.isfinite(o[1]).all() and torch.isfinite(lse[1]).all()
 
 
 def test_decode_equals_the_contiguous_varlen_decode():
@@ -454,19 +519,44 @@ def test_select_and_sparse_decode(lens, Hq, Hkv, D, P, w0, W, sink, top_k, mode)
     _check_decode(o, lse, q, k, v, table, lens, w0, W, 1e6, mode, lists=kept)
 
 
-def test_select_ties_go_to_the_lowest_page():
-    P, L, D = 16, 16 * 1000, 64
-    s = torch.zeros(1000, 2, D, dtype=BF16, device=DEV)  # every score is zero, of either sign
+@pytest.mark.parametrize("n", [1000, 5000, 20000])  # one, two and eight CTAs per row
+def test_select_ties_go_to_the_lowest_page(n):
+    P, D = 16, 64
+    s = torch.zeros(n, 2, D, dtype=BF16, device=DEV)  # every score is zero, of either sign
     g = torch.Generator().manual_seed(0)
     q = _randn(g, 1, 4, D)
-    table = torch.arange(1000, dtype=torch.int32, device=DEV)[None]
-    lst, cnt, err = _select(q, s, table, [L], P, 0, 4000, 2, 600, 1e4)
-    assert err == 0 and cnt.tolist() == [[603, 603]]
-    assert lst[0, 0].tolist() == list(range(602)) + [999]
+    table = torch.arange(n, dtype=torch.int32, device=DEV)[None]
+    top = 600 * n // 1000
+    lst, cnt, err = _select(q, s, table, [P * n], P, 0, 4000, 2, top, 1e4)
+    assert err == 0 and cnt.tolist() == [[top + 3, top + 3]]
+    assert lst[0, 0].tolist() == list(range(top + 2)) + [n - 1]
     # a NaN summary scores above everything, and in one head only
-    s[700, 1, 3] = float("nan")
-    lst, cnt, _ = _select(q, s, table, [L], P, 0, 4000, 2, 600, 1e4)
-    assert lst[0, 1].tolist() == list(range(601)) + [700, 999] and lst[0, 0].tolist() == list(range(602)) + [999]
+    s[n - 300, 1, 3] = float("nan")
+    lst, cnt, _ = _select(q, s, table, [P * n], P, 0, 4000, 2, top, 1e4)
+    assert lst[0, 1].tolist() == list(range(top + 1)) + [n - 300, n - 1]
+    assert lst[0, 0].tolist() == list(range(top + 2)) + [n - 1]
+
+
+@pytest.mark.parametrize("kind", ["plain", "large", "tiny", "equal", "close"])
+@pytest.mark.parametrize("pages,Hq,Hkv,D,top_k", [(3000, 4, 1, 128, 100), (70000, 2, 2, 64, 900), (9000, 8, 1, 64, 5)])
+def test_select_where_the_error_bound_decides(kind, pages, Hq, Hkv, D, top_k):
+    # scores that the first pass tells apart, lengths beyond its range, lengths below it,
+    # summaries that are all the same, and summaries one rounding step apart
+    g = torch.Generator().manual_seed(pages)
+    P, L = 16, 16 * pages
+    scale = {"plain": 0.25, "large": 1e6, "tiny": 1e-9}.get(kind, 1.0)
+    s = _randn(g, pages, Hkv, D, scale=scale)
+    if kind in ("equal", "close"):
+        s = s[:1].expand(pages, Hkv, D).contiguous()
+    if kind == "close":
+        s *= torch.where(torch.rand(pages, Hkv, D, generator=g) < 0.5, 1.0, 1.0 + 2.0 ** -7).to(BF16).to(DEV)
+    q = _randn(g, 1, Hq, D)
+    table = torch.randperm(pages, generator=g).to(torch.int32).to(DEV)[None]
+    # with w_pretrained 8 the pages share few positions, and equal summaries score alike
+    W = 8 if kind in ("equal", "close") else L // 5
+    lst, cnt, err = _select(q, s, table, [L], P, 200, W, 3, top_k, 1e6)
+    assert err == 0
+    _check_lists(lst, cnt, q, s, table, [L], P, 200, W, 3, top_k, 1e6)
 
 
 def test_select_flags_bad_lengths_and_pages():
@@ -565,6 +655,79 @@ def test_prompt_and_decode_steps_across_a_group_border():
         _check_decode(od, ld, qs, k, v, table, lens, w0, W, base, lists=kept)
         assert int(err) == 0
     assert {2, 3, 4} <= seen
+
+
+def test_a_captured_step_serves_other_lengths():
+    # append, summaries, selection and both decodes in one graph, replayed as sequences grow
+    # and end; a padded slot carries length 0 and position -1
+    B, Hq, Hkv, D, P, M = 3, 8, 2, 64, 16, 30
+    W, w0, base = 100, 30, 1e4
+    g = torch.Generator().manual_seed(5)
+    k, v = _pool(g, B * M, P, Hkv, D)
+    table = torch.randperm(B * M, generator=g).view(B, M).to(torch.int32).to(DEV)
+    s = _randn(g, B * M, Hkv, D, scale=0.25)
+    x, w = _randn(g, B, Hq + 2 * Hkv, D), _randn(g, D)
+    seq, pos, lens = _i32([0, 1, 2]), _i32([0, 0, 0]), _i32([1, 1, 1])
+    q, od, os_ = (torch.zeros(B, Hq, D, dtype=BF16, device=DEV) for _ in range(3))
+    ld, ls = (torch.zeros(B, Hq, device=DEV) for _ in range(2))
+    lst, cnt = torch.zeros(B, Hkv, 8, dtype=torch.int32, device=DEV), torch.zeros(B, Hkv, dtype=torch.int32, device=DEV)
+    ws, err = _ws(Hq, Hkv, D), _i32([0])
+    sel = torch.zeros(jl.jl_select_pages_workspace_bytes(B, Hkv, M), dtype=torch.uint8, device=DEV)
+    rule = dict(w0=w0, w_pretrained=W, rope_base=base, dev_error=err)
+
+    def step():
+        jl.jl_qk_norm_rope_append_paged(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], w, w, seq, pos, table, q, k, v,
+                                        eps=ph.EPS, rope_base=base, dev_error=err)
+        jl.jl_page_summaries(k, table, pos.clamp(min=0), lens, s, max_new=1, rope_base=base, dev_error=err)
+        jl.jl_select_pages(q, s, table, lens, lst, cnt, page_size=P, sink_pages=1, top_k=4, workspace=sel, **rule)
+        jl.jl_bifocal_decode_paged_sparse(q, k, v, table, lens, lst, cnt, os_, ls, workspace=ws, **rule)
+        jl.jl_bifocal_decode_paged(q, k, v, table, lens, od, ld, workspace=ws, **rule)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for now in ([450, 1, 300], [451, 0, 301], [16, 17, 479]):
+        lens.copy_(_i32(now))
+        pos.copy_(_i32([n - 1 for n in now]))
+        x.copy_(_randn(g, B, Hq + 2 * Hkv, D))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        _check_decode(od, ld, q, k, v, table, now, w0, W, base)
+        kept = _check_lists(lst, cnt, q, s, table, now, P, w0, W, 1, 4, base)
+        _check_decode(os_, ls, q, k, v, table, now, w0, W, base, lists=kept)
+
+
+def test_two_streams_with_their_own_workspaces():
+    g = torch.Generator().manual_seed(31)
+    P, Hq, Hkv, D = 16, 8, 2, 128
+    k, v = _pool(g, 1300, P, Hkv, D)
+    cases = []
+    for lens in ([9000, 5], [300, 11000]):
+        table = _table(g, lens, P, 1300)
+        cases.append((lens, table, _randn(g, 2, Hq, D), _i32(lens)))
+    want = []
+    for lens, table, q, sl in cases:
+        o, lse = torch.empty_like(q), torch.empty(2, Hq, device=DEV)
+        jl.jl_bifocal_decode_paged(q, k, v, table, sl, o, lse, w0=50, w_pretrained=2000, rope_base=1e6,
+                                   workspace=_ws(Hq, Hkv, D))
+        want.append((o, lse))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [_ws(Hq, Hkv, D), _ws(Hq, Hkv, D)]
+    outs = [(torch.empty_like(c[2]), torch.empty(2, Hq, device=DEV)) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (lens, table, q, sl), st, ws, (o, lse) in zip(cases, streams, spaces, outs):
+            jl.jl_bifocal_decode_paged(q, k, v, table, sl, o, lse, w0=50, w_pretrained=2000, rope_base=1e6,
+                                       workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    for (o, lse), (wo, wl) in zip(outs, want):
+        assert torch.equal(o, wo) and torch.equal(lse, wl)
 
 
 def test_outputs_stay_inside_their_buffers():
