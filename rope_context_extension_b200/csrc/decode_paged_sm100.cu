@@ -210,20 +210,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   Entry* ent = reinterpret_cast<Entry*>(smem + C::kEntOff);  // the warps' heads (2 w) and tails (2 w + 1)
 
-  bool any_empty, any_large;
+  // ---- what needs no memory: barriers, key factors
+  if (tid < kWarps * S) {
+    mbar_init(smem_addr(smem + C::kBarOff) + 8 * tid, 1);
+    fence_mbar_init();
+  }
   if (tid == 0) {
     tma_prefetch_map(&tm_k);
     tma_prefetch_map(&tm_v);
-  }
-  // ---- how much there is to do, and where this CTA's and this warp's share is
-  const int per_seg = (items + kSegs - 1) / kSegs;
-  if (tid < kWarps * S) mbar_init(smem_addr(smem + C::kBarOff) + 8 * tid, 1);
-  if (tid == 0) {
-    fence_mbar_init();
     *abort_flag = 0;
     scan[0] = 0;
   }
   if (tid < 2 * kWarps) ent[tid].item = -1;
+  constexpr int kRowsAtOnce = D == 128 ? 1 : 2;  // rows of R(-e) that a warp's lanes cover
+  for (int e = kRowsAtOnce * warp + (D == 128 ? 0 : lane >> 4); e < C::kERows; e += kRowsAtOnce * kWarps) {
+    float4 f;
+    sincos_phase(-e, turn0, &f.z, &f.x);
+    sincos_phase(-e, turn1, &f.w, &f.y);
+    *reinterpret_cast<float4*>(smem + C::kEOff + e * C::kERow + qt * 8) = f;
+  }
+
+  // ---- how much there is to do, and where this CTA's and this warp's share is
+  const int per_seg = (items + kSegs - 1) / kSegs;
+  bool any_empty, any_large;
   {
     int64_t v = 0;
     bool none = false, large = false;
@@ -495,257 +504,244 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   // The step behind the last unit closes the last segment.
 #pragma unroll 1
-  for (int k = -1; k <= cnt; ++k) {
-    if (k == -1) {
-      // The first units are on their way; meanwhile the CTA forms its tables.
-      constexpr int kRowsAtOnce = D == 128 ? 1 : 2;  // rows of R(-e) that a warp's lanes cover
-      for (int e = kRowsAtOnce * warp + (D == 128 ? 0 : lane >> 4); e < C::kERows; e += kRowsAtOnce * kWarps) {
-        float4 f;
-        sincos_phase(-e, turn0, &f.z, &f.x);
-        sincos_phase(-e, turn1, &f.w, &f.y);
-        *reinterpret_cast<float4*>(smem + C::kEOff + e * C::kERow + qt * 8) = f;
+  for (int k = 0; k <= cnt; ++k) {
+    int4 md = make_int4(-1, -1, 0, 0);
+    if (k < cnt) md = meta[k % C::kMeta];
+    if (cnt == 0) break;
+    if (md.x != item) {
+      if (item >= 0) {  // the segment in hand ends here
+        const bool began = seg_k >= seg_c;
+        const int64_t first = wb + seg_k - seg_c;
+        const int n = k == cnt || !began ? item_units(a, item) : 0;
+        const bool ends = k < cnt || first + n <= we;
+        if (began && ends) {
+          store_final(item);
+        } else if (k < cnt) {  // begun before this warp's range
+          store_partial(partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + warp, part_floats));
+          if (lane == 0) ent[2 * warp] = {first, n, item};
+        } else {  // ends with the range or runs on; the warp's ring is free for it
+          store_partial(partial_at(reinterpret_cast<float*>(smem), warp, S * C::kSlot / 4));
+          if (lane == 0) ent[2 * warp + 1] = {first, n, item};
+        }
       }
-      __syncthreads();
+      if (k == cnt) break;
+      item = md.x;
+      seg_c = md.z;
+      seg_k = k;
+      m_used = -INFINITY;
+      l_part = 0.f;
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) oacc[n][0] = oacc[n][1] = oacc[n][2] = oacc[n][3] = 0.f;
+      const int b = item / a.Hkv, g = item - b * a.Hkv;
+      L = a.seq_lens[b];
+      // (group_size, query_remote and query_shift in 32 bits; 64-bit divisions are what a
+      // segment's start would spend its time on)
+      G = (int)((unsigned)(L - 1) / (unsigned)a.w_pretrained) + 1;
+      all_local = jl::all_local(L, a.w0, G);
+      dq = all_local ? 0 : (L - 1) / G + (a.qshift == 1 ? a.w0 - a.w0 / G : 0) - (L - 1);
+      g_inv = 0xffffffffu / (unsigned)G;
+      jb = -1;
+      local_from = all_local ? 0 : L - a.w0;  // keys j >= local_from are scored with base RoPE
+      const __nv_bfloat16* qp = a.q + ((int64_t)b * a.Hq + g * r + hq) * D + 2 * c4;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        qf[ks][0] = hq < r ? *reinterpret_cast<const uint32_t*>(qp + 16 * ks) : 0u;
+        qf[ks][1] = hq < r ? *reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8) : 0u;
+      }
     }
-    if (k >= 0) {
-      int4 md = make_int4(-1, -1, 0, 0);
-      if (k < cnt) md = meta[k % C::kMeta];
-      if (cnt == 0) break;
-      if (md.x != item) {
-        if (item >= 0) {  // the segment in hand ends here
-          const bool began = seg_k >= seg_c;
-          const int64_t first = wb + seg_k - seg_c;
-          const int n = k == cnt || !began ? item_units(a, item) : 0;
-          const bool ends = k < cnt || first + n <= we;
-          if (began && ends) {
-            store_final(item);
-          } else if (k < cnt) {  // begun before this warp's range
-            store_partial(partial_at(a.warp_parts, (int64_t)blockIdx.x * kWarps + warp, part_floats));
-            if (lane == 0) ent[2 * warp] = {first, n, item};
-          } else {  // ends with the range or runs on; the warp's ring is free for it
-            store_partial(partial_at(reinterpret_cast<float*>(smem), warp, S * C::kSlot / 4));
-            if (lane == 0) ent[2 * warp + 1] = {first, n, item};
-          }
-        }
-        if (k == cnt) break;
-        item = md.x;
-        seg_c = md.z;
-        seg_k = k;
-        m_used = -INFINITY;
-        l_part = 0.f;
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) oacc[n][0] = oacc[n][1] = oacc[n][2] = oacc[n][3] = 0.f;
-        const int b = item / a.Hkv, g = item - b * a.Hkv;
-        L = a.seq_lens[b];
-        // (group_size, query_remote and query_shift in 32 bits; 64-bit divisions are what a
-        // segment's start would spend its time on)
-        G = (int)((unsigned)(L - 1) / (unsigned)a.w_pretrained) + 1;
-        all_local = jl::all_local(L, a.w0, G);
-        dq = all_local ? 0 : (L - 1) / G + (a.qshift == 1 ? a.w0 - a.w0 / G : 0) - (L - 1);
-        g_inv = 0xffffffffu / (unsigned)G;
-        jb = -1;
-        local_from = all_local ? 0 : L - a.w0;  // keys j >= local_from are scored with base RoPE
-        const __nv_bfloat16* qp = a.q + ((int64_t)b * a.Hq + g * r + hq) * D + 2 * c4;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          qf[ks][0] = hq < r ? *reinterpret_cast<const uint32_t*>(qp + 16 * ks) : 0u;
-          qf[ks][1] = hq < r ? *reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8) : 0u;
-        }
+    const int j0 = md.y;
+    const bool any_local = all_local || j0 + 15 >= local_from;
+    const bool any_remote = !all_local && j0 < local_from;
+    uint32_t ef[2] = {0u, 0u};  // factor rows of this lane's keys hrow and 8 + hrow
+    if (j0 >= 0 && any_remote) {
+      // floor(j0 / G) by floor((2^32 - 1) / G): at most one short
+      int qd = (int)__umulhi((unsigned)j0, g_inv), rm = j0 - qd * G;
+      if (rm >= G) {
+        rm -= G;
+        ++qd;
       }
-      const int j0 = md.y;
-      const bool any_local = all_local || j0 + 15 >= local_from;
-      const bool any_remote = !all_local && j0 < local_from;
-      uint32_t ef[2] = {0u, 0u};  // factor rows of this lane's keys hrow and 8 + hrow
-      if (j0 >= 0 && any_remote) {
-        // floor(j0 / G) by floor((2^32 - 1) / G): at most one short
-        int qd = (int)__umulhi((unsigned)j0, g_inv), rm = j0 - qd * G;
-        if (rm >= G) {
-          rm -= G;
-          ++qd;
-        }
-        // Turned queries serve while the keys' own turns from where they were formed,
-        // e = (j0 + u - jb) - (floor((j0 + u) / G) - floor(jb / G)), stay in the table.
-        int off = (j0 - jb) - (qd - qb);
-        if (jb < 0 || j0 < jb || off > C::kERows - 16) {
-          jb = j0;
-          qb = qd;
-          off = 0;
-          float4 f;
-          sincos_phase(dq - (qd - j0), turn0, &f.z, &f.x);
-          sincos_phase(dq - (qd - j0), turn1, &f.w, &f.y);
-          __syncwarp();
-          *reinterpret_cast<float4*>(smem + C::kCsOff + warp * D * 4 + qt * 8) = f;  // (D = 64: twice the same)
-          __syncwarp();
-          // packed heads sit in two lanes each: either turns every other k-step
+      // Turned queries serve while the keys' own turns from where they were formed,
+      // e = (j0 + u - jb) - (floor((j0 + u) / G) - floor(jb / G)), stay in the table.
+      int off = (j0 - jb) - (qd - qb);
+      if (jb < 0 || j0 < jb || off > C::kERows - 16) {
+        jb = j0;
+        qb = qd;
+        off = 0;
+        float4 f;
+        sincos_phase(dq - (qd - j0), turn0, &f.z, &f.x);
+        sincos_phase(dq - (qd - j0), turn1, &f.w, &f.y);
+        __syncwarp();
+        *reinterpret_cast<float4*>(smem + C::kCsOff + warp * D * 4 + qt * 8) = f;  // (D = 64: twice the same)
+        __syncwarp();
+        // packed heads sit in two lanes each: either turns every other k-step
 #pragma unroll
-          for (int i = 0; i < (kPack ? KS2 / 2 : KS2); ++i) {
-            const int kp = kPack ? 2 * i + (hrow >> 2) : i;
-            uint32_t q0, q1, q2, q3;
-            if (kPack) {  // qf[kp], qf[kp + KS2] without indexing registers
-              q0 = hrow < 4 ? qf[2 * i][0] : qf[2 * i + 1][0];
-              q1 = hrow < 4 ? qf[2 * i][1] : qf[2 * i + 1][1];
-              q2 = hrow < 4 ? qf[2 * i + KS2][0] : qf[2 * i + 1 + KS2][0];
-              q3 = hrow < 4 ? qf[2 * i + KS2][1] : qf[2 * i + 1 + KS2][1];
+        for (int i = 0; i < (kPack ? KS2 / 2 : KS2); ++i) {
+          const int kp = kPack ? 2 * i + (hrow >> 2) : i;
+          uint32_t q0, q1, q2, q3;
+          if (kPack) {  // qf[kp], qf[kp + KS2] without indexing registers
+            q0 = hrow < 4 ? qf[2 * i][0] : qf[2 * i + 1][0];
+            q1 = hrow < 4 ? qf[2 * i][1] : qf[2 * i + 1][1];
+            q2 = hrow < 4 ? qf[2 * i + KS2][0] : qf[2 * i + 1 + KS2][0];
+            q3 = hrow < 4 ? qf[2 * i + KS2][1] : qf[2 * i + 1 + KS2][1];
+          } else {
+            q0 = qf[i][0], q1 = qf[i][1], q2 = qf[i + KS2][0], q3 = qf[i + KS2][1];
+          }
+          uint4 lo, hi;
+          rot_split_neg(q0, q2, csb[8 * kp + c4], lo.x, lo.y, hi.x, hi.y);
+          rot_split_neg(q1, q3, csb[8 * kp + 4 + c4], lo.z, lo.w, hi.z, hi.w);
+          qbuf[(kp * 2) * kQLanes + qlane] = lo;
+          qbuf[(kp * 2 + 1) * kQLanes + qlane] = hi;
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int u = 8 * i + hrow;
+        const int x = rm + u;  // below G + 16
+        int qe = (int)__umulhi((unsigned)x, g_inv);
+        if (x - qe * G >= G) ++qe;
+        ef[i] = sbase + C::kEOff + (off + u - qe) * C::kERow + c4 * 16;
+      }
+    }
+    h_next = 2 * k;
+    if (!wait()) break;
+    const uint32_t kst = ring + slot * C::kSlot + tile_off;
+    float x[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    if (j0 >= 0) {
+      // This lane's scores: keys 8 nt + 2 c4 + {0, 1} of head hq.  A unit on the
+      // band's edge forms both kinds and each key keeps its own.
+      if (any_remote) {
+        // hi and (negated) lo parts of the keys in accumulators of their own, of the
+        // queries in rows h and h + 8: the four add up to (q_hi + q_lo) . (k_hi + k_lo)
+        float sah[2][4], sal[2][4];
+#pragma unroll
+        for (int kp = 0; kp < KS2; ++kp) {
+          // k-step kp holds the first coordinate of pairs t in [16 kp, 16 kp + 16), k-step
+          // kp + D/32 the second, so each pair is complete in registers
+          uint32_t klo[4], khi[4], kah[4], kal[4], kbh[4], kbl[4], alo[4], ahi[4];
+          load_keys<D>(kst, kp, klo);
+          load_keys<D>(kst, kp + KS2, khi);
+          lds_u4(qaddr + (kp * 2) * kQLanes * 16, alo);
+          lds_u4(qaddr + (kp * 2 + 1) * kQLanes * 16, ahi);
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            float4 f01, f23;
+            lds_f4(ef[nt] + kp * 128, f01);
+            lds_f4(ef[nt] + kp * 128 + 64, f23);
+            rot_split_neg(klo[2 * nt], khi[2 * nt], f01, kah[2 * nt], kal[2 * nt], kbh[2 * nt], kbl[2 * nt]);
+            rot_split_neg(klo[2 * nt + 1], khi[2 * nt + 1], f23, kah[2 * nt + 1], kal[2 * nt + 1],
+                           kbh[2 * nt + 1], kbl[2 * nt + 1]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            if (kp == 0) {
+              mma_bf16_first(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
+              mma_bf16_first(sal[nt], alo, kal[2 * nt], kal[2 * nt + 1]);
             } else {
-              q0 = qf[i][0], q1 = qf[i][1], q2 = qf[i + KS2][0], q3 = qf[i + KS2][1];
+              mma_bf16(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
+              mma_bf16(sal[nt], alo, kal[2 * nt], kal[2 * nt + 1]);
             }
-            uint4 lo, hi;
-            rot_split_neg(q0, q2, csb[8 * kp + c4], lo.x, lo.y, hi.x, hi.y);
-            rot_split_neg(q1, q3, csb[8 * kp + 4 + c4], lo.z, lo.w, hi.z, hi.w);
-            qbuf[(kp * 2) * kQLanes + qlane] = lo;
-            qbuf[(kp * 2 + 1) * kQLanes + qlane] = hi;
+            mma_bf16(sah[nt], ahi, kbh[2 * nt], kbh[2 * nt + 1]);
+            mma_bf16(sal[nt], ahi, kbl[2 * nt], kbl[2 * nt + 1]);
           }
-          __syncwarp();
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int u = 8 * i + hrow;
-          const int x = rm + u;  // below G + 16
-          int qe = (int)__umulhi((unsigned)x, g_inv);
-          if (x - qe * G >= G) ++qe;
-          ef[i] = sbase + C::kEOff + (off + u - qe) * C::kERow + c4 * 16;
-        }
-      }
-      h_next = 2 * k;
-      if (!wait()) break;
-      const uint32_t kst = ring + slot * C::kSlot + tile_off;
-      float x[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-      if (j0 >= 0) {
-        // This lane's scores: keys 8 nt + 2 c4 + {0, 1} of head hq.  A unit on the
-        // band's edge forms both kinds and each key keeps its own.
-        if (any_remote) {
-          // hi and (negated) lo parts of the keys in accumulators of their own, of the
-          // queries in rows h and h + 8: the four add up to (q_hi + q_lo) . (k_hi + k_lo)
-          float sah[2][4], sal[2][4];
-#pragma unroll
-          for (int kp = 0; kp < KS2; ++kp) {
-            // k-step kp holds the first coordinate of pairs t in [16 kp, 16 kp + 16), k-step
-            // kp + D/32 the second, so each pair is complete in registers
-            uint32_t klo[4], khi[4], kah[4], kal[4], kbh[4], kbl[4], alo[4], ahi[4];
-            load_keys<D>(kst, kp, klo);
-            load_keys<D>(kst, kp + KS2, khi);
-            lds_u4(qaddr + (kp * 2) * kQLanes * 16, alo);
-            lds_u4(qaddr + (kp * 2 + 1) * kQLanes * 16, ahi);
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              float4 f01, f23;
-              lds_f4(ef[nt] + kp * 128, f01);
-              lds_f4(ef[nt] + kp * 128 + 64, f23);
-              rot_split_neg(klo[2 * nt], khi[2 * nt], f01, kah[2 * nt], kal[2 * nt], kbh[2 * nt], kbl[2 * nt]);
-              rot_split_neg(klo[2 * nt + 1], khi[2 * nt + 1], f23, kah[2 * nt + 1], kal[2 * nt + 1],
-                             kbh[2 * nt + 1], kbl[2 * nt + 1]);
-            }
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              if (kp == 0) {
-                mma_bf16_first(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
-                mma_bf16_first(sal[nt], alo, kal[2 * nt], kal[2 * nt + 1]);
-              } else {
-                mma_bf16(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
-                mma_bf16(sal[nt], alo, kal[2 * nt], kal[2 * nt + 1]);
-              }
-              mma_bf16(sah[nt], ahi, kbh[2 * nt], kbh[2 * nt + 1]);
-              mma_bf16(sal[nt], ahi, kbl[2 * nt], kbl[2 * nt + 1]);
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              x[nt][e] = (sah[nt][e] - sah[nt][e + 2]) - (sal[nt][e] - sal[nt][e + 2]);
-        }
-        if (any_local) {  // base query, keys as stored
-          float sb[2][4];
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sb[nt][e] = 0.f;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            uint32_t kk[4];
-            load_keys<D>(kst, ks, kk);
-            const uint32_t aq[4] = {qf[ks][0], 0u, qf[ks][1], 0u};
-            mma_bf16(sb[0], aq, kk[0], kk[1]);
-            mma_bf16(sb[1], aq, kk[2], kk[3]);
-          }
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (!any_remote || j0 + 8 * nt + 2 * c4 + e >= local_from) x[nt][e] = sb[nt][e];
-        }
-      }
-      pass_on(2 * k);
-      h_next = 2 * k + 1;
-      if (!wait()) break;
-      if (j0 >= 0) {
-        const uint32_t vst = ring + slot * C::kSlot + tile_off;
-        // log2 units, the mask behind the sequence, and the running maximum of the lane's head
-        const bool tail = j0 + 16 > L;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            x[nt][e] *= sl2;
-            if (tail && j0 + 8 * nt + 2 * c4 + e >= L) x[nt][e] = -INFINITY;
-          }
-        float mt = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-        const bool grow = mt > m_used + 8.f;  // a maximum up to 2^8 behind keeps every p below 2^8
-        if (__any_sync(0xffffffffu, grow)) {
-          const float alpha = grow ? ex2_approx(m_used - mt) : 1.f;  // 0 for the first keys
-          l_part *= alpha;
-          if (grow) m_used = mt;
-          // this lane's O^T columns are heads 2 c4 and 2 c4 + 1 (and, packed, their lo parts)
-          const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c4);
-          const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * c4 + 4);
+          for (int e = 0; e < 2; ++e)
+            x[nt][e] = (sah[nt][e] - sah[nt][e + 2]) - (sal[nt][e] - sal[nt][e + 2]);
+      }
+      if (any_local) {  // base query, keys as stored
+        float sb[2][4];
 #pragma unroll
-          for (int n = 0; n < D / 16; ++n) {
-            oacc[n][0] *= a0;
-            oacc[n][1] *= a1;
-            oacc[n][2] *= a0;
-            oacc[n][3] *= a1;
-          }
-        }
-        const float msub = (m_used == -INFINITY) ? 0.f : m_used;
-        uint32_t ph[2], pl[2];  // P^T fragments are the lane's own scores
+        for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const float p0 = ex2_approx(x[nt][0] - msub), p1 = ex2_approx(x[nt][1] - msub);
-          l_part += p0 + p1;
-          if (kPack)
-            split_neg_bf16(f2_pack(p0, p1), ph[nt], pl[nt]);
-          else
-            split_f2_bf16(f2_pack(p0, p1), ph[nt], pl[nt]);
-        }
-        const uint32_t pb0 = kPack && hrow >= 4 ? pl[0] : ph[0];
-        const uint32_t pb1 = kPack && hrow >= 4 ? pl[1] : ph[1];
-        // rows behind the sequence hold anything, NaN included
-        uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
-        if (tail) {
-          const int u = L - j0 - 2 * c4;  // of the keys 2 c4 + {0, 1} and 8 + 2 c4 + {0, 1}
-          vm0 = (u > 0 ? 0xffffu : 0u) | (u > 1 ? 0xffff0000u : 0u);
-          vm1 = (u > 8 ? 0xffffu : 0u) | (u > 9 ? 0xffff0000u : 0u);
+          for (int e = 0; e < 4; ++e) sb[nt][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t kk[4];
+          load_keys<D>(kst, ks, kk);
+          const uint32_t aq[4] = {qf[ks][0], 0u, qf[ks][1], 0u};
+          mma_bf16(sb[0], aq, kk[0], kk[1]);
+          mma_bf16(sb[1], aq, kk[2], kk[3]);
         }
 #pragma unroll
-        for (int mt2 = 0; mt2 < D / 16; ++mt2) {
-          const uint32_t addr = (vst ^ ((mt2 & 3) << 5)) + (mt2 >> 2) * 2048;
-          uint32_t va[4];
-          ldsm_x4_t(addr, va[0], va[1], va[2], va[3]);
-          if (tail) {
-            va[0] &= vm0;
-            va[1] &= vm0;
-            va[2] &= vm1;
-            va[3] &= vm1;
-          }
-          mma_bf16(oacc[mt2], va, pb0, pb1);
-          if (!kPack) mma_bf16(oacc[mt2], va, pl[0], pl[1]);
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (!any_remote || j0 + 8 * nt + 2 * c4 + e >= local_from) x[nt][e] = sb[nt][e];
+      }
+    }
+    pass_on(2 * k);
+    h_next = 2 * k + 1;
+    if (!wait()) break;
+    if (j0 >= 0) {
+      const uint32_t vst = ring + slot * C::kSlot + tile_off;
+      // log2 units, the mask behind the sequence, and the running maximum of the lane's head
+      const bool tail = j0 + 16 > L;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[nt][e] *= sl2;
+          if (tail && j0 + 8 * nt + 2 * c4 + e >= L) x[nt][e] = -INFINITY;
+        }
+      float mt = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+      const bool grow = mt > m_used + 8.f;  // a maximum up to 2^8 behind keeps every p below 2^8
+      if (__any_sync(0xffffffffu, grow)) {
+        const float alpha = grow ? ex2_approx(m_used - mt) : 1.f;  // 0 for the first keys
+        l_part *= alpha;
+        if (grow) m_used = mt;
+        // this lane's O^T columns are heads 2 c4 and 2 c4 + 1 (and, packed, their lo parts)
+        const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c4);
+        const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * c4 + 4);
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          oacc[n][0] *= a0;
+          oacc[n][1] *= a1;
+          oacc[n][2] *= a0;
+          oacc[n][3] *= a1;
         }
       }
-      pass_on(2 * k + 1);
-      __syncwarp();  // a description may have been written
+      const float msub = (m_used == -INFINITY) ? 0.f : m_used;
+      uint32_t ph[2], pl[2];  // P^T fragments are the lane's own scores
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const float p0 = ex2_approx(x[nt][0] - msub), p1 = ex2_approx(x[nt][1] - msub);
+        l_part += p0 + p1;
+        if (kPack)
+          split_neg_bf16(f2_pack(p0, p1), ph[nt], pl[nt]);
+        else
+          split_f2_bf16(f2_pack(p0, p1), ph[nt], pl[nt]);
+      }
+      const uint32_t pb0 = kPack && hrow >= 4 ? pl[0] : ph[0];
+      const uint32_t pb1 = kPack && hrow >= 4 ? pl[1] : ph[1];
+      // rows behind the sequence hold anything, NaN included
+      uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
+      if (tail) {
+        const int u = L - j0 - 2 * c4;  // of the keys 2 c4 + {0, 1} and 8 + 2 c4 + {0, 1}
+        vm0 = (u > 0 ? 0xffffu : 0u) | (u > 1 ? 0xffff0000u : 0u);
+        vm1 = (u > 8 ? 0xffffu : 0u) | (u > 9 ? 0xffff0000u : 0u);
+      }
+#pragma unroll
+      for (int mt2 = 0; mt2 < D / 16; ++mt2) {
+        const uint32_t addr = (vst ^ ((mt2 & 3) << 5)) + (mt2 >> 2) * 2048;
+        uint32_t va[4];
+        ldsm_x4_t(addr, va[0], va[1], va[2], va[3]);
+        if (tail) {
+          va[0] &= vm0;
+          va[1] &= vm0;
+          va[2] &= vm1;
+          va[3] &= vm1;
+        }
+        mma_bf16(oacc[mt2], va, pb0, pb1);
+        if (!kPack) mma_bf16(oacc[mt2], va, pl[0], pl[1]);
+      }
     }
+    pass_on(2 * k + 1);
+    __syncwarp();  // a description may have been written
   }
   if (!ok) {
     // Gave up at half unit h_next: let the copies in flight land (again with a limit)

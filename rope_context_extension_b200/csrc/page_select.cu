@@ -252,7 +252,6 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const __gr
   constexpr int kWarps = kScoreThreads / 32;
   constexpr int kRow = ScoreSmem<D>::kRow;
   extern __shared__ __align__(16) uint8_t score_smem[];
-  asm volatile("griddepcontrol.launch_dependents;");  // the selection may take its place; it waits for the scores
   ScoreSmem<D>& sm = *reinterpret_cast<ScoreSmem<D>*>(score_smem);
   const int b = blockIdx.y;
   const PageSpan sp = page_span(a, b);
@@ -466,7 +465,6 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(const __grid_c
   __shared__ uint32_t rkey[kRank];
   __shared__ float wmax[kWarps];
   const int CL = gridDim.x, rank = blockIdx.x;  // the cluster is the grid's x
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // all that was launched before is done
   const int g = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = (int64_t)b * a.Hkv + g;
@@ -821,15 +819,13 @@ cudaError_t launch_page_select(PageSelectArgs& a, int D, cudaStream_t stream) {
   cfg.gridDim = dim3(cl, a.Hkv, a.B);
   cfg.blockDim = dim3(kSelThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cl;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   const PageSelectArgs& ca = a;
   return D == 128 ? cudaLaunchKernelEx(&cfg, page_select_kernel<128>, ca)
                   : cudaLaunchKernelEx(&cfg, page_select_kernel<64>, ca);
