@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (__any_sync(0xffffffffu, open)) {
         cur_it += 32;
         cur_s += tot;
-        if (cur_it >= items) break;  // cannot happen while lengths stay as they were scanned
+        if (cur_it >= items) break;  // (only if a length changed under the call: no unit, no bad address)
       } else {  // the next batch begins in or behind the last unit's item
         const int last = min(31, cnt - 1 - k0);
         cur_it = __shfl_sync(0xffffffffu, my_it, last);
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     m_j0 = -1;
     m_row = 0;
     m_c = 0;
-    m_item = my_it;
+    m_item = max(my_it, 0);
     if (valid && my_it >= 0) {
       const int b = my_it / a.Hkv;
       const int c = (int)(x - my_s);
@@ -849,7 +849,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* wts = reinterpret_cast<float*>(smem + C::kWtsOff);  // [r][kMaxParts]
   float* part_l = wts + kMaxR * C::kMaxParts;                 // [r][kMaxParts] the parts' sums
   float* tot = part_l + kMaxR * C::kMaxParts;                 // [r] maxima, then [r] sums
-  auto cta_of = [&](int64_t unit) -> int { return (int)div_units((unit + 1) * N - 1, U); };
+  auto cta_of = [&](int64_t unit) -> int {
+    return (int)min(max(div_units((unit + 1) * N - 1, U), (int64_t)0), N - 1);
+  };
   __threadfence();
   __syncthreads();
   if (tid < 2 && (tid == 0 ? shared_item[0] : shared_item[1]) >= 0) {

@@ -27,7 +27,9 @@ int shape_checks(int B, int Hq, int Hkv, int D, double rope_base) {
 
 int rule_checks(int w0, int w_pretrained, int mode) {
   if (w0 < 0 || w_pretrained < 1) return JL_ERR_INVALID_ARG;
-  if (mode != JL_QSHIFT_NONE && mode != JL_QSHIFT_SELF_EXTEND) return JL_ERR_INVALID_ARG;
+  // the prefill flags mean nothing here, as in the other decode calls
+  if ((mode & ~(JL_QSHIFT_SELF_EXTEND | JL_PREFILL_FP16 | JL_PREFILL_KEYS_IN_KERNEL)) != 0) return JL_ERR_INVALID_ARG;
+  if ((mode & JL_PREFILL_FP16) && (mode & JL_PREFILL_KEYS_IN_KERNEL)) return JL_ERR_INVALID_ARG;
   return JL_OK;
 }
 
@@ -205,7 +207,7 @@ int decode_paged(const void* q, const jl_paged_kv* cache, const int32_t* block_t
   a.r = Hq / Hkv;
   a.w0 = w0;
   a.w_pretrained = w_pretrained;
-  a.qshift = mode;
+  a.qshift = mode & JL_QSHIFT_SELF_EXTEND;
   a.scale_log2 = jl::resolve_scale(softmax_scale, D) * 1.4426950408889634f;
   std::memcpy(a.turn, jl::turn_table(D, rope_base).fixed, sizeof(a.turn));
   if (jl::launch_decode_paged(tk, tv, a, D, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
@@ -361,7 +363,7 @@ int jl_select_pages(const void* q, const void* summaries, int64_t num_pages, int
   a.r = Hq / Hkv;
   a.w0 = w0;
   a.w_pretrained = w_pretrained;
-  a.qshift = mode;
+  a.qshift = mode & JL_QSHIFT_SELF_EXTEND;
   a.sink_pages = sink_pages;
   a.top_k = top_k;
   a.dev_error = dev_error;

@@ -251,6 +251,25 @@ def test_decode_ratios_and_layouts(r, layout):
     _check_decode(o, lse, q, k, v, table, lens, 50, 400, 1e6, scale=0.2)
 
 
+def test_sequences_that_share_their_first_pages():
+    g = torch.Generator().manual_seed(17)
+    lens, P, Hq, Hkv, D = [400, 333, 320], 16, 8, 2, 128
+    k, v = _pool(g, 70, P, Hkv, D)
+    table = _table(g, lens, P, 70, width=25)
+    table[1:, :20] = table[0, :20]  # 320 positions in common
+    q = _randn(g, 3, Hq, D)
+    o, lse = torch.empty_like(q), torch.empty(3, Hq, device=DEV)
+    jl.jl_bifocal_decode_paged(q, k, v, table, _i32(lens), o, lse, w0=30, w_pretrained=100, rope_base=1e6,
+                               workspace=_ws(Hq, Hkv, D))
+    _check_decode(o, lse, q, k, v, table, lens, 30, 100, 1e6)
+    s = torch.zeros(70, Hkv, D, dtype=BF16, device=DEV)
+    jl.jl_page_summaries(k, table, _i32([0, 0, 0]), _i32(lens), s, max_new=400, rope_base=1e6)
+    alone = torch.zeros_like(s)
+    for b in range(3):
+        jl.jl_page_summaries(k, table[b:b + 1], _i32([0]), _i32(lens[b:b + 1]), alone, max_new=400, rope_base=1e6)
+    assert torch.equal(s, alone)
+
+
 def test_decode_with_outlier_keys_and_one_dominant_key():
     g = torch.Generator().manual_seed(9)
     lens, P, Hq, Hkv, D = [3000], 16, 8, 2, 128

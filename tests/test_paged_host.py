@@ -113,7 +113,8 @@ def test_decode_refusals(lib):
     for name in ("bt", "lens", "lse"):
         assert _decode(lib, **{name: A + 2}) == ALIGNMENT, name
     assert _decode(lib, w0=-1) == INVALID and _decode(lib, W=0) == INVALID and _decode(lib, mode=2) == INVALID
-    assert _decode(lib, mode=jl.JL_PREFILL_FP16) == INVALID
+    assert _decode(lib, mode=jl.JL_PREFILL_FP16, ws=None) == WORKSPACE  # ignored, as in the other decode calls
+    assert _decode(lib, mode=jl.JL_PREFILL_FP16 | jl.JL_PREFILL_KEYS_IN_KERNEL) == INVALID
     assert _decode(lib, scale=float("nan")) == INVALID
     assert _decode(lib, Hq=18) == UNSUPPORTED  # nine queries per KV head
     assert _decode(lib, B=65536) == UNSUPPORTED
@@ -142,7 +143,7 @@ def test_select_refusals(lib):
     assert _select(lib, M=100, w0=33, sink=1, k=2, stride=6) == INVALID  # 1 + 2 + ceil(33 / 16) + 1 = 7
     assert _select(lib, Hq=18) == UNSUPPORTED
     assert _select(lib, ws=None) == WORKSPACE and _select(lib, ws_bytes=8) == WORKSPACE
-    assert _select(lib, mode=4) == INVALID
+    assert _select(lib, mode=2) == INVALID
 
 
 def test_workspace_sizes(lib):
