@@ -78,9 +78,10 @@ struct PgCfg {
   static constexpr int kMiscOff = kMetaOff + kWarps * kMeta * 16;
   static constexpr int kEntOff = kMiscOff + 16;    // the warps' partials: items, first units, sizes
   static constexpr int kSmem = kEntOff + 32 * kWarps + 1024;
-  static constexpr int kWtsOff = kQOff;            // the joins' weights; the query fragments are done with
-  static constexpr int kMaxParts = 256;            // parts that one join weighs: CTAs of a device, warps of a CTA
-  static_assert((2 * kMaxR * kMaxParts + 2 * kMaxR) * 4 <= kWarps * kQBytes, "room for the weights");
+  static constexpr int kMaxParts = 256;            // parts that one join weighs: CTAs of a device
+  static constexpr int kWtsFloats = 2 * kMaxR * kMaxParts + 2 * kMaxR;
+  static constexpr int kWtsOff = kThreads * 16;    // two joins' weights behind their sums; the rings are done with
+  static_assert(kWtsOff + 2 * kWtsFloats * 4 <= kRing, "room for the weights");
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -157,6 +158,13 @@ __device__ __forceinline__ void load_keys(uint32_t tile, int ks, uint32_t (&k)[4
   ldsm_x4((tile ^ ((ks & 3) << 5)) + (ks >> 2) * 2048, k[0], k[1], k[2], k[3]);
 }
 
+// atomicInc with release and acquire at the device's scope.
+__device__ __forceinline__ unsigned atomic_inc_acq_rel(unsigned* p, unsigned last) {
+  unsigned old;
+  asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(last) : "memory");
+  return old;
+}
+
 // A partial result: 8 maxima (log2 units), 8 sums, [r][D] outputs.
 struct Partial {
   float* m;
@@ -202,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* scan = reinterpret_cast<int64_t*>(smem + C::kScanOff);
   volatile int* misc = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
   volatile int* abort_flag = misc;               // [0]
-  volatile int* ticket = misc + 1;               // [1], [2]: whether this CTA joins the item it shares
+  volatile int* ticket = misc + 1;               // [1], [2]: whether this CTA joins the item it shares (none: 0)
   struct Entry {
     int64_t s;  // the item's first unit
     int n;      // its units
@@ -846,36 +854,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (shared_item[0] < 0 && shared_item[1] < 0) return;  // the same for every thread of the CTA
 
   // ---- join the CTAs' partials: the item's last ticket does it
-  float* wts = reinterpret_cast<float*>(smem + C::kWtsOff);  // [r][kMaxParts]
-  float* part_l = wts + kMaxR * C::kMaxParts;                 // [r][kMaxParts] the parts' sums
-  float* tot = part_l + kMaxR * C::kMaxParts;                 // [r] maxima, then [r] sums
   auto cta_of = [&](int64_t unit) -> int {
     return (int)min(max(div_units((unit + 1) * N - 1, U), (int64_t)0), N - 1);
   };
-  __threadfence();
+  // The barrier orders the CTA's partials before the ticket, and the ticket after it
+  // what the joining CTA reads: one thread's release and acquire cover them all.
   __syncthreads();
+  if (tid < 2) ticket[tid] = 0;
   if (tid < 2 && (tid == 0 ? shared_item[0] : shared_item[1]) >= 0) {
     const int64_t s = tid == 0 ? shared_s[0] : shared_s[1];
     const int first = cta_of(s), behind = cta_of(s + (tid == 0 ? shared_n[0] : shared_n[1]) - 1) - first;
-    ticket[tid] = atomicInc(&a.counters[first], (unsigned)behind) == (unsigned)behind;
+    ticket[tid] = atomic_inc_acq_rel(&a.counters[first], (unsigned)behind) == (unsigned)behind;
   }
   __syncthreads();
+  // Where both items are this CTA's to join (the slowest CTA's as a rule), half of the
+  // warps take either, as long as half of them hold an item's r D / 4 columns.
+  const int cols = r * D / 4;
+  const bool both = ticket[0] != 0 && ticket[1] != 0 && 2 * cols <= kThreads;
+  const int side = both && warp >= kWarps / 2 ? 1 : 0;
+  const int nw = both ? kWarps / 2 : kWarps, tw = warp - side * nw, t = tid - side * 32 * nw;
+  float* wts = reinterpret_cast<float*>(smem + C::kWtsOff) + side * C::kWtsFloats;  // [r][kMaxParts]
+  float* part_l = wts + kMaxR * C::kMaxParts;                 // [r][kMaxParts] the parts' sums
+  float* tot = part_l + kMaxR * C::kMaxParts;                 // [r] maxima, then [r] sums
+  float4* sums = reinterpret_cast<float4*>(smem) + side * 32 * nw;  // [groups][cols]
 #pragma unroll 1
-  for (int slot = 0; slot < 2; ++slot) {
-    const int it = shared_item[slot];
-    if (it < 0 || ticket[slot] == 0) continue;  // the same for every thread of the CTA
-    const int first = cta_of(shared_s[slot]), last = cta_of(shared_s[slot] + shared_n[slot] - 1);
-    __threadfence();
+  for (int pass = 0; pass < (both ? 1 : 2); ++pass) {
+    const int slot = both ? side : pass;
+    if (ticket[slot] == 0) continue;  // the same for every thread of the CTA
+    const int it = slot == 0 ? shared_item[0] : shared_item[1];
+    const int64_t s = slot == 0 ? shared_s[0] : shared_s[1];
+    const int first = cta_of(s), last = cta_of(s + (slot == 0 ? shared_n[0] : shared_n[1]) - 1);
     const int n = last - first + 1;
     // the item begins inside the first CTA's range (slot 1) and before the others' (slot 0)
     const int64_t step = 2 * part_floats;
     const float* parts = a.cta_parts + first * step;
     // Thread groups take every groups-th part of four dims, then their sums meet in unit
     // order; the first parts are on their way while the weights are formed.
-    const int cols = r * D / 4, groups = kThreads / cols;
-    const int grp = tid / cols, idx = 4 * (tid - grp * cols);
+    const int groups = 32 * nw / cols;
+    const int grp = t / cols, idx = 4 * (t - grp * cols);
     const float* po = parts + 2 * kMaxR + idx;
-    constexpr int kEarly = 4;
+    constexpr int kEarly = 8;
     float4 early[kEarly];
 #pragma unroll
     for (int i = 0; i < kEarly; ++i) {
@@ -884,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (grp < groups && c < n)
         early[i] = __ldcg(reinterpret_cast<const float4*>(po + c * step + (c == 0 ? part_floats : 0)));
     }
-    for (int h = warp; h < r; h += kWarps) {  // weights, one warp per head
+    for (int h = tw; h < r; h += nw) {  // weights, one warp per head
       float* w = wts + h * C::kMaxParts;
       float M = -INFINITY, l = 0.f;
       for (int c = lane; c < n; c += 32) {
@@ -909,7 +927,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncthreads();
-    float4* sums = reinterpret_cast<float4*>(smem);  // [groups][cols]; the rings are done with
     if (grp < groups) {
       const float* w = wts + (idx / D) * C::kMaxParts;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
