@@ -36,6 +36,15 @@
 // pairs too (2^-17; one bf16 would double the output's own rounding error): for up
 // to four heads, duplicated in M rows 4-7, the lo parts use the columns 4-7 of the
 // P V product, which would be idle.
+//
+// Measured (B200, 32 query and 8 KV heads, D 128, w0 4096, G 4; replayed graphs):
+// one sequence of 131072 keys 97-98 us = 5.5 TB/s, 0.84 of a copy; eight of them
+// 665-755 us = 5.7-6.5 TB/s by the clock that the power limit leaves (1.0004 bytes of
+// DRAM per byte needed).  The fixed part is about 16 us: 4.5 us to the first keys,
+// 1.5 us for the warps' join, 6 us for tickets and the CTAs' join; the issue slots are
+// 57% busy, with the keys' turn and split the most of it.  64 sequences of up to 8192
+// keys (16 heads): 166 us, 0.90.  A sparse step of eight sequences, 97 pages of 64 keys
+// per KV head: 50 us.  777 keys of one D = 64 head: 12.4 us, all latency.
 #include "jl_mma.cuh"
 #include "jl_paged.cuh"
 
@@ -45,13 +54,7 @@ namespace {
 
 constexpr int kSegs = 128;  // runs of items whose unit counts the CTA scans
 
-#ifndef JL_PG_WARPS
-#define JL_PG_WARPS 12
-#endif
-#ifndef JL_PG_SLOTS
-#define JL_PG_SLOTS 3
-#endif
-constexpr int kWarps = JL_PG_WARPS;
+constexpr int kWarps = 12;  // 168 registers each; 16 of 128 spill (4 sequences of 128K: 561 instead of 418 us then)
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMinUnits = kWarps;  // units per CTA below which fewer CTAs share a call's work
 // Items that warps take whole: up to 4 units always, up to 8 where there are at least
@@ -63,7 +66,9 @@ constexpr int kMaxR = 8;
 template <int D>
 struct PgCfg {
   static constexpr int kSlot = 16 * D * 2;         // bytes of a unit's keys, or of its values
-  static constexpr int kSlots = JL_PG_SLOTS * (128 / D);  // ring depth of a warp: keys, values, keys, ...
+  // Ring depth of a warp: keys, values, keys, ...  (12 KB per warp, 144 KB per SM in
+  // flight; two or four tiles of D = 128 measured the same)
+  static constexpr int kSlots = 3 * (128 / D);
   static constexpr int kMeta = 4;                  // units described ahead (a power of two)
   static constexpr int kRing = kWarps * kSlots * kSlot;
   static constexpr int kERow = D * 4 + 64;         // bytes per row of the key factors (padded)
