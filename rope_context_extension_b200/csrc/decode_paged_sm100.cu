@@ -39,7 +39,7 @@
 //
 // Measured (B200, 32 query and 8 KV heads, D 128, w0 4096, G 4; replayed graphs):
 // one sequence of 131072 keys 97-98 us = 5.5 TB/s, 0.84 of a copy; eight of them
-// 665-755 us = 5.7-6.5 TB/s by the clock that the power limit leaves (1.0004 bytes of
+// 665-755 us = 5.7-6.5 TB/s by the clock that the power limit leaves (1.0003 bytes of
 // DRAM per byte needed).  The fixed part is about 16 us: 4.5 us to the first keys,
 // 1.5 us for the warps' join, 6 us for tickets and the CTAs' join; the issue slots are
 // 57% busy, with the keys' turn and split the most of it.  64 sequences of up to 8192
