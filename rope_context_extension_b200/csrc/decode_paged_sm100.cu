@@ -83,10 +83,14 @@ struct PgCfg {
   static constexpr int kMiscOff = kMetaOff + kWarps * kMeta * 16;
   static constexpr int kEntOff = kMiscOff + 16;    // the warps' partials: items, first units, sizes
   static constexpr int kSmem = kEntOff + 32 * kWarps + 1024;
-  static constexpr int kMaxParts = 256;            // parts that one join weighs: CTAs of a device
+  static constexpr int kMaxParts = 160;            // parts that one join weighs: the grid's bound
+  static constexpr int kChunk = 8;                 // parts that one thread adds up in one go
+  static constexpr int kMaxChunks = kMaxParts / kChunk;
   static constexpr int kWtsFloats = 2 * kMaxR * kMaxParts + 2 * kMaxR;
-  static constexpr int kWtsOff = kThreads * 16;    // two joins' weights behind their sums; the rings are done with
-  static_assert(kWtsOff + 2 * kWtsFloats * 4 <= kRing, "room for the weights");
+  static constexpr int kWtsOff = kQOff;            // two joins' weights; the query fragments are done with
+  static_assert(2 * kWtsFloats * 4 <= kWarps * kQBytes, "room for the weights");
+  // the chunks' sums of one join of up to 8 D / 4 columns, or of two that share the threads, in the rings
+  static_assert(kMaxChunks * (2 * D > kThreads ? 2 * D : kThreads) * 16 <= kRing, "room for the sums");
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -881,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* wts = reinterpret_cast<float*>(smem + C::kWtsOff) + side * C::kWtsFloats;  // [r][kMaxParts]
   float* part_l = wts + kMaxR * C::kMaxParts;                 // [r][kMaxParts] the parts' sums
   float* tot = part_l + kMaxR * C::kMaxParts;                 // [r] maxima, then [r] sums
-  float4* sums = reinterpret_cast<float4*>(smem) + side * 32 * nw;  // [groups][cols]
+  float4* sums = reinterpret_cast<float4*>(smem) + side * C::kMaxChunks * cols;  // [chunks][cols]
 #pragma unroll 1
   for (int pass = 0; pass < (both ? 1 : 2); ++pass) {
     const int slot = both ? side : pass;
@@ -893,20 +897,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the item begins inside the first CTA's range (slot 1) and before the others' (slot 0)
     const int64_t step = 2 * part_floats;
     const float* parts = a.cta_parts + first * step;
-    // Thread groups take every groups-th part of four dims, then their sums meet in unit
-    // order; the first parts are on their way while the weights are formed.
-    const int groups = 32 * nw / cols;
+    // Chunks of parts add up in unit order, and so do the chunks: the same sums for any
+    // number of threads.  The first chunk is on its way while the weights are formed.
+    const int chunks = (n + C::kChunk - 1) / C::kChunk, groups = 32 * nw / cols;
     const int grp = t / cols, idx = 4 * (t - grp * cols);
     const float* po = parts + 2 * kMaxR + idx;
-    constexpr int kEarly = 8;
-    float4 early[kEarly];
+    float4 v[C::kChunk];
+    auto load_chunk = [&](int ch) {
 #pragma unroll
-    for (int i = 0; i < kEarly; ++i) {
-      const int c = grp + i * groups;
-      early[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (grp < groups && c < n)
-        early[i] = __ldcg(reinterpret_cast<const float4*>(po + c * step + (c == 0 ? part_floats : 0)));
-    }
+      for (int i = 0; i < C::kChunk; ++i) {
+        const int c = ch * C::kChunk + i;
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < n) v[i] = __ldcg(reinterpret_cast<const float4*>(po + c * step + (c == 0 ? part_floats : 0)));
+      }
+    };
+    if (grp < groups) load_chunk(grp);
     for (int h = tw; h < r; h += nw) {  // weights, one warp per head
       float* w = wts + h * C::kMaxParts;
       float M = -INFINITY, l = 0.f;
@@ -934,19 +939,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (grp < groups) {
       const float* w = wts + (idx / D) * C::kMaxParts;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int ch = grp; ch < chunks; ch += groups) {
+        if (ch != grp) load_chunk(ch);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kEarly; ++i)
-        if (grp + i * groups < n) add(o, w[grp + i * groups], early[i]);
-#pragma unroll 4
-      for (int c = grp + kEarly * groups; c < n; c += groups)
-        add(o, w[c], __ldcg(reinterpret_cast<const float4*>(po + c * step)));
-      sums[grp * cols + idx / 4] = o;
+        for (int i = 0; i < C::kChunk; ++i)
+          if (ch * C::kChunk + i < n) add(o, w[ch * C::kChunk + i], v[i]);
+        sums[ch * cols + idx / 4] = o;
+      }
     }
     __syncthreads();
     if (grp == 0) {
       float4 o = sums[idx / 4];
-      for (int i = 1; i < groups; ++i) add(o, 1.f, sums[i * cols + idx / 4]);
+      for (int i = 1; i < chunks; ++i) add(o, 1.f, sums[i * cols + idx / 4]);
       write_result(row_of(it), idx, o, tot[idx / D], tot[kMaxR + idx / D]);
     }
     __syncthreads();  // the shared buffers may be written again

@@ -418,6 +418,26 @@ def test_decode_runs_are_equal_bit_for_bit():
     assert all(torch.equal(o, got[0][0]) and torch.equal(x, got[0][1]) for o, x in got)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,lens", [(32, 8, 128, [3000, 2900, 3100, 50]), (8, 8, 64, [5000, 4100, 600, 77]),
+                                           (24, 3, 128, [9000, 2000, 4000, 8000]), (6, 2, 64, [20000, 30000, 9, 1000]),
+                                           (32, 8, 128, [1500, 1400, 1300, 1200, 1100, 1600, 1700, 1250])])
+def test_decode_sums_do_not_depend_on_which_cta_comes_last(Hq, Hkv, D, lens):
+    # Items that several CTAs share, most CTAs two of them: which CTA joins what, and
+    # whether one joins both its items, changes from run to run; the results do not.
+    g = torch.Generator().manual_seed(18)
+    P, need = 16, sum((x + 15) // 16 for x in lens) + 8
+    k, v = _pool(g, need, P, Hkv, D)
+    table = _table(g, lens, P, need)
+    q = _randn(g, len(lens), Hq, D)
+    ws, n = _ws(Hq, Hkv, D), _i32(lens)
+    o = torch.empty(300, *q.shape, dtype=q.dtype, device=DEV)
+    lse = torch.empty(300, len(lens), Hq, device=DEV)
+    for i in range(300):
+        jl.jl_bifocal_decode_paged(q, k, v, table, n, o[i], lse[i], w0=500, w_pretrained=3000, rope_base=1e6,
+                                   workspace=ws)
+    assert (o == o[0]).all() and (lse == lse[0]).all()
+
+
 def test_decode_graph_serves_other_lengths_and_streams():
     g = torch.Generator().manual_seed(10)
     P, Hq, Hkv, D = 32, 8, 2, 128
