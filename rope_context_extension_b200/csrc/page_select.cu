@@ -23,21 +23,12 @@ namespace jl {
 namespace {
 
 constexpr int kSumThreads = 256;
-constexpr int kSumBlocksPerSm = 2;  // resident (three spill: 54 against 52 us for 2048 pages of 64 keys, 8 heads)
+constexpr int kSumBlocksPerSm = 2;  // resident (three of two passes each: 57 against 48.7 us for 2048 pages of 64 keys)
 constexpr int kScoreThreads = 256;
 constexpr int kMaxTile = 256;       // pages per CTA of the score kernel, at most
 constexpr int kHeadBlock = 8;       // KV heads whose turned queries a CTA of the score kernel holds
 constexpr int kSelThreads = 512;
 constexpr int kRank = 128;          // pages between the edges that are ranked by comparing all
-
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16lo_to_f32(u[i]);
-    x[2 * i + 1] = bf16hi_to_f32(u[i]);
-  }
-}
 
 // cos and sin of n theta, theta / 2 pi in 64-bit fixed point as sincos_phase takes
 // it, the phase's sine and cosine to fp32.
@@ -50,12 +41,13 @@ __device__ __forceinline__ void sincos_fixed(int n, uint64_t turn, float* s, flo
 }
 
 // One warp per (page, KV head).  A key row takes D/16 lanes of two 16-byte loads, a
-// warp reads 512 / D rows at a time and kAhead such passes before it sums them, and
+// warp reads 512 / D rows at a time, loads kAhead such passes while it sums the kAhead
+// before (two: 60 us, three: 52, four: 48.7, for 2048 pages of 64 keys), and
 // each group of lanes sums its rows by Horner's rule in R(-step): sum_i R(-step i)
 // k_{step i + grp}, so that two fixed rotations per lane, formed once per warp, serve
 // every page.  Memory bound: a page's keys are read once (2048 pages of 64 keys, 8
-// heads, D 128: 52-54 us = 5.1 TB/s, 0.77 of a copy, of which the launch, the factors
-// and the uneven end are about 7 us; 8 single pages 4.1 us).
+// heads, D 128: 48.7 us = 5.6 TB/s, 0.85 of a copy; four times as many 175 us = 6.2
+// TB/s; 8 single pages 4.1 us).
 template <int D>
 __global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm)
     page_summary_kernel(const __grid_constant__ PageSummaryArgs a) {
@@ -67,12 +59,18 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm)
   const int lane = threadIdx.x & 31;
   const int sub = lane % kLanes, grp = lane / kLanes;
   const int P = a.pages.page_size;
-  float sc[8], ss[8];  // R(-step)
+  uint64_t sc[4], ss[4];  // R(-step), packed pairs
   {
     const uint64_t* tp = a.turn;  // a generic read: an indexed parameter read serialises
     asm volatile("" : "+l"(tp));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sincos_fixed(-kStep, tp[8 * sub + e], &ss[e], &sc[e]);
+    for (int e = 0; e < 4; ++e) {
+      float s0, c0, s1, c1;
+      sincos_fixed(-kStep, tp[8 * sub + 2 * e], &s0, &c0);
+      sincos_fixed(-kStep, tp[8 * sub + 2 * e + 1], &s1, &c1);
+      ss[e] = f2_pack(s0, s1);
+      sc[e] = f2_pack(c0, c1);
+    }
     for (int i = threadIdx.x; i < kStep * (H2 / 2); i += kSumThreads) {
       const int row = i / (H2 / 2), t = i % (H2 / 2);
       float4 f;
@@ -110,48 +108,72 @@ __global__ void __launch_bounds__(kSumThreads, kSumBlocksPerSm)
     if (!ok) {
       if (lane == 0 && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
     } else if (start < L && lp <= (L - 1) / P) {
-      next_n = min(P, L - lp * P);
       next_phys = a.block_table[(int64_t)b * a.max_pages + lp];
+      if (next_phys >= 0 && next_phys < a.pages.num_pages)
+        next_n = min(P, L - lp * P);
+      else if (lane == 0 && a.dev_error)
+        atomicExch(a.dev_error, kDevBadLength);
     }
   };
+  // A batch of kAhead passes, from row r0 down, loaded while the one before is summed,
+  // the next task's first batch while a task's last one is.
+  uint4 next_lo[kAhead], next_hi[kAhead];
+  auto load = [&](int phys, int g, int n, int r0) {
+    const __nv_bfloat16* base =
+        a.pages.k + phys * a.pages.page_stride + g * a.pages.head_stride + grp * a.pages.row_stride + 8 * sub;
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const int row = r0 - s * kStep;
+      next_lo[s] = next_hi[s] = make_uint4(0, 0, 0, 0);
+      if (row >= 0 && row + grp < n) {
+        next_lo[s] = *reinterpret_cast<const uint4*>(base + row * a.pages.row_stride);
+        next_hi[s] = *reinterpret_cast<const uint4*>(base + row * a.pages.row_stride + H2);
+      }
+    }
+  };
+  auto load_first = [&]() {
+    if (next_n > 0) load(next_phys, next_g, next_n, (next_n - 1) / kStep * kStep);
+  };
   describe(task);
+  load_first();
   for (; task < tasks; task += nwarps) {
     const int n = next_n, phys = next_phys, g = next_g;
     describe(task + nwarps);
-    if (n == 0) continue;
-    if (phys < 0 || phys >= a.pages.num_pages) {
-      if (lane == 0 && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
+    if (n == 0) {
+      load_first();
       continue;
     }
-    const __nv_bfloat16* base =
-        a.pages.k + phys * a.pages.page_stride + g * a.pages.head_stride + grp * a.pages.row_stride + 8 * sub;
-    float x[8], y[8];
+    uint64_t x2[4], y2[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
+    for (int e = 0; e < 4; ++e) x2[e] = y2[e] = 0ull;
     for (int r0 = (n - 1) / kStep * kStep; r0 >= 0; r0 -= kAhead * kStep) {
       uint4 lo[kAhead], hi[kAhead];
 #pragma unroll
       for (int s = 0; s < kAhead; ++s) {
-        const int row = r0 - s * kStep;
-        lo[s] = hi[s] = make_uint4(0, 0, 0, 0);
-        if (row >= 0 && row + grp < n) {
-          lo[s] = *reinterpret_cast<const uint4*>(base + row * a.pages.row_stride);
-          hi[s] = *reinterpret_cast<const uint4*>(base + row * a.pages.row_stride + H2);
-        }
+        lo[s] = next_lo[s];
+        hi[s] = next_hi[s];
       }
+      if (r0 >= kAhead * kStep)
+        load(phys, g, n, r0 - kAhead * kStep);
+      else
+        load_first();
 #pragma unroll
       for (int s = 0; s < kAhead; ++s) {
         if (r0 - s * kStep < 0) break;
-        float kx[8], ky[8];
-        unpack8(lo[s], kx);
-        unpack8(hi[s], ky);
+        const uint32_t kx[4] = {lo[s].x, lo[s].y, lo[s].z, lo[s].w}, ky[4] = {hi[s].x, hi[s].y, hi[s].z, hi[s].w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float xr = kx[e] + (x[e] * sc[e] - y[e] * ss[e]);
-          y[e] = ky[e] + (y[e] * sc[e] + x[e] * ss[e]);
-          x[e] = xr;
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t xr = f2_sub(f2_fma(x2[e], sc[e], bf16x2_to_f2(kx[e])), f2_mul(y2[e], ss[e]));
+          y2[e] = f2_fma(x2[e], ss[e], f2_fma(y2[e], sc[e], bf16x2_to_f2(ky[e])));
+          x2[e] = xr;
         }
       }
+    }
+    float x[8], y[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f2_unpack(x2[e], x[2 * e], x[2 * e + 1]);
+      f2_unpack(y2[e], y[2 * e], y[2 * e + 1]);
     }
     const float inv = 1.f / (float)n;
 #pragma unroll
