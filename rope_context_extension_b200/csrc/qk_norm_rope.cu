@@ -13,15 +13,15 @@
 // of a row's first half and the 8 that pair with them in the second (two 16-byte
 // loads), so a row takes D/16 lanes, the sum of squares takes log2(D/16)
 // shuffles, and no value crosses lanes for the rotation.  A warp handles 512 / D
-// rows at a time, the next ones already on their way, and a slice of one token's
-// heads per task; the token's D/2 factors are formed once per task, two per lane,
+// rows at a time, the next ones already on their way, across tasks too, and a slice of
+// one token's heads per task; the token's D/2 factors are formed once per task, two per lane,
 // and shared through shared memory (64-bit fixed-point angles and the MUFU's sine:
 // 2^-21, against the result's 2^-8).
 //
 // Measured (B200, 32 query and 8 KV heads, D 128): a prompt of 131072 tokens appended
-// to its pages 518 us = 6.2 TB/s, 0.95 of a copy; 8192 tokens without an append 33.4
-// us = 5.0 TB/s, 0.77 (the launch, the first loads and the uneven end are about 7 us;
-// DRAM 45% and issue slots 72% busy under the profiler); 8 tokens 3.2 us, all latency.
+// to its pages 518 us = 6.2 TB/s, 0.95 of a copy; 8192 tokens without an append 32.5
+// us = 5.2 TB/s, 0.79 (the launch, the first loads and the uneven end are about 5 us);
+// 8 tokens 3.2 us, all latency.
 #include <algorithm>
 
 #include "jl_mma.cuh"
@@ -62,40 +62,57 @@ __global__ void __launch_bounds__(kNrThreads, kBlocksPerSm) norm_rope_kernel(con
   const int heads = a.Hq + a.Hkv + (a.v != nullptr ? a.Hkv : 0);
   const int64_t tasks = (int64_t)a.T * a.tasks_per_token;
   const int64_t nwarps = (int64_t)gridDim.x * (kNrThreads / 32);
-  for (int64_t task = (int64_t)blockIdx.x * (kNrThreads / 32) + warp; task < tasks; task += nwarps) {
-    const int64_t tok = a.tasks_per_token == 1 ? task : task / a.tasks_per_token;
-    const int slice = (int)(task - tok * a.tasks_per_token);
-    const int h0 = slice * a.heads_per_task, h1 = min(heads, h0 + a.heads_per_task);
-    // a pass's rows: loaded one pass ahead
-    uint4 lo, hi, next_lo, next_hi;
-    auto load = [&](int h) {
-      next_lo = next_hi = make_uint4(0, 0, 0, 0);
-      if (h < h1) {
-        const __nv_bfloat16* src = h < a.Hq ? a.q + tok * a.q_stride + (int64_t)h * D
-                                   : h < a.Hq + a.Hkv
-                                       ? a.k + tok * a.k_stride + (int64_t)(h - a.Hq) * D
-                                       : a.v + tok * a.v_stride + (int64_t)(h - a.Hq - a.Hkv) * D;
-        next_lo = *reinterpret_cast<const uint4*>(src + 8 * sub);
-        next_hi = *reinterpret_cast<const uint4*>(src + H2 + 8 * sub);
-      }
-    };
-    load(h0 + grp);
-    const int pos = a.positions[tok];
-    if (pos == -1) continue;  // a padded token
-    bool bad = pos < 0;
-    int64_t kv_base = 0;  // offset of the token's row in the pages, head 0
+  int64_t task = (int64_t)blockIdx.x * (kNrThreads / 32) + warp;
+  // The next task: its token, heads, position and row in the pages (head 0), looked up
+  // while the task before is worked on; next_h0 = next_h1: none.
+  int next_tok = 0, next_h0 = 0, next_h1 = 0, next_pos = -1;
+  int64_t next_base = 0;
+  auto describe = [&](int64_t t) {
+    next_h0 = next_h1 = 0;
+    next_pos = -1;
+    if (t >= tasks) return;
+    next_tok = (int)(a.tasks_per_token == 1 ? t : t / a.tasks_per_token);
+    next_h0 = (int)(t - (int64_t)next_tok * a.tasks_per_token) * a.heads_per_task;
+    next_h1 = min(heads, next_h0 + a.heads_per_task);
+    next_pos = a.positions[next_tok];
+    if (next_pos == -1) return;  // a padded token
+    bool bad = next_pos < 0;
     if (a.v != nullptr) {
-      const int sq = a.seq_ids[tok];
-      bad = bad || sq < 0 || sq >= a.B || (int64_t)pos >= a.max_pages * a.pages.page_size;
+      const int sq = a.seq_ids[next_tok];
+      bad = bad || sq < 0 || sq >= a.B || (int64_t)next_pos >= a.max_pages * a.pages.page_size;
       if (!bad) {
-        const int lp = pos / a.pages.page_size;
+        const int lp = next_pos / a.pages.page_size;
         const int page = a.block_table[(int64_t)sq * a.max_pages + lp];
         bad = page < 0 || page >= a.pages.num_pages;
-        kv_base = page * a.pages.page_stride + (int64_t)(pos - lp * a.pages.page_size) * a.pages.row_stride;
+        next_base = page * a.pages.page_stride + (int64_t)(next_pos - lp * a.pages.page_size) * a.pages.row_stride;
       }
     }
     if (bad) {
       if (lane == 0 && a.dev_error) atomicExch(a.dev_error, kDevBadLength);
+      next_pos = -1;
+    }
+  };
+  // a pass's rows: loaded one pass ahead, a task's first while the last of the task before is worked on
+  uint4 lo, hi, next_lo, next_hi;
+  auto load = [&](int64_t tok, int h, int h1) {
+    next_lo = next_hi = make_uint4(0, 0, 0, 0);
+    if (h < h1) {
+      const __nv_bfloat16* src = h < a.Hq ? a.q + tok * a.q_stride + (int64_t)h * D
+                                 : h < a.Hq + a.Hkv
+                                     ? a.k + tok * a.k_stride + (int64_t)(h - a.Hq) * D
+                                     : a.v + tok * a.v_stride + (int64_t)(h - a.Hq - a.Hkv) * D;
+      next_lo = *reinterpret_cast<const uint4*>(src + 8 * sub);
+      next_hi = *reinterpret_cast<const uint4*>(src + H2 + 8 * sub);
+    }
+  };
+  describe(task);
+  load(next_tok, next_h0 + grp, next_h1);
+  for (; task < tasks; task += nwarps) {
+    const int64_t tok = next_tok, kv_base = next_base;
+    const int h0 = next_h0, h1 = next_h1, pos = next_pos;
+    describe(task + nwarps);
+    if (pos < 0) {
+      load(next_tok, next_h0 + grp, next_h1);
       continue;
     }
     {
@@ -110,7 +127,10 @@ __global__ void __launch_bounds__(kNrThreads, kBlocksPerSm) norm_rope_kernel(con
       const int h = hb + grp;
       lo = next_lo;
       hi = next_hi;
-      load(h + kRows);
+      if (hb + kRows < h1)
+        load(tok, h + kRows, h1);
+      else
+        load(next_tok, next_h0 + grp, next_h1);
       const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
       const int hk = h - a.Hq - (is_v ? a.Hkv : 0);
       uint64_t x[4], y[4];  // packed fp32 pairs: half the instructions, which bound short rows
@@ -175,13 +195,14 @@ cudaError_t launch_d(NormRopeArgs& a, cudaStream_t stream) {
   if (sms == 0) return cudaErrorNoDevice;
   const int heads = a.Hq + a.Hkv + (a.v != nullptr ? a.Hkv : 0);
   const int passes = (heads + kRows - 1) / kRows;
-  // Passes per task: what keeps the resident warps' last round full, counting two
-  // passes' time for a task's own start (position, page, factors).
+  // Passes per task: what keeps the resident warps' last round full, counting half a
+  // pass for a task's own start (4096 tokens 18.6 us, with two passes 19.5, four 19.5 and
+  // 8192 tokens 34.7 instead of 32.5).
   const int64_t warps = (int64_t)sms * kBlocksPerSm * (kNrThreads / 32);
   int64_t best = INT64_MAX;
   for (int per = 1; per <= passes; ++per) {
     const int each = (passes + per - 1) / per;
-    const int64_t cost = (((int64_t)a.T * each + warps - 1) / warps) * (per + 2);
+    const int64_t cost = (((int64_t)a.T * each + warps - 1) / warps) * (2 * per + 1);
     if (cost < best) {
       best = cost;
       a.heads_per_task = per * kRows;
