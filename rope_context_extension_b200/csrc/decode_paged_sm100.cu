@@ -30,15 +30,17 @@
 // that starts at position j0 has dk(j) = dk(j0) - e(j) with e(j) in [0, 15]: the
 // queries take R(dq - dk(j0)), whose D/2 factors the warp's lanes form once per
 // unit, and the keys take R(-e) from a 16-row table, in registers.  Corrected
-// operands enter the products as bf16 hi + lo pairs (about 16 significant bits;
-// one bf16 would put 2^-9 |q| |k| on a score), the queries' lo parts in the M rows
-// 8-15 that at most eight heads leave free.  Probabilities are carried as hi + lo
+// operands enter the products as fp16 hi + lo pairs (about 22 significant bits; bf16
+// pairs, 17 bits, put an error of 1.6e-6 on the log-sum of rows that one large key
+// dominates), the queries' lo parts in the M rows 8-15 that at most eight heads leave
+// free.  Keys or queries beyond fp16's range are found by their scores and scored again
+// in fp32.  Probabilities are carried as hi + lo
 // pairs too (2^-17; one bf16 would double the output's own rounding error): for up
 // to four heads, duplicated in M rows 4-7, the lo parts use the columns 4-7 of the
 // P V product, which would be idle.
 //
 // Measured (B200, 32 query and 8 KV heads, D 128, w0 4096, G 4; replayed graphs):
-// one sequence of 131072 keys 97-98 us = 5.5 TB/s, 0.84 of a copy; eight of them
+// one sequence of 131072 keys 98-99 us = 5.4 TB/s, 0.83 of a copy; eight of them
 // 665-755 us = 5.7-6.5 TB/s by the clock that the power limit leaves (1.0003 bytes of
 // DRAM per byte needed).  The fixed part is about 16 us: 4.5 us to the first keys,
 // 1.5 us for the warps' join, 6 us for tickets and the CTAs' join; the issue slots are
@@ -62,6 +64,10 @@ constexpr int kMinUnits = kWarps;  // units per CTA below which fewer CTAs share
 // -> 21.0 us).
 constexpr int kWholeUnits = 4, kWholeUnitsMany = 8;
 constexpr int kMaxR = 8;
+// Turned operands are scaled by powers of two on their way to fp16: an entry of a key (a
+// query) is off by at most 2^-22 of itself or 2^-31 (2^-29), whichever is more, up to
+// 1000 (4000), where fp16 ends.  What lies beyond takes another path.
+constexpr float kKeyScale = 64.f, kQueryScale = 16.f, kUnscale = 1.f / (kKeyScale * kQueryScale);
 
 template <int D>
 struct PgCfg {
@@ -131,9 +137,9 @@ __device__ __forceinline__ void lds_u4(uint32_t addr, uint32_t (&v)[4]) {
 }
 
 // The first product of a sum.
-__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
@@ -151,14 +157,28 @@ __device__ __forceinline__ void split_neg_bf16(uint64_t v, uint32_t& hi, uint32_
   lo = pack_bf16x2(ra, rb);
 }
 
+__device__ __forceinline__ void split_neg_f16(uint64_t v, uint32_t& hi, uint32_t& lo) {
+  float a, b, ra, rb;
+  f2_unpack(v, a, b);
+  hi = pack_f16x2(a, b);
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tsub.rn.f32.f16 %0, l, %3;\n\tsub.rn.f32.f16 %1, h, %4;\n\t}"
+      : "=f"(ra), "=f"(rb)
+      : "r"(hi), "f"(a), "f"(b));
+  lo = pack_f16x2(ra, rb);
+}
+
 // The bf16 pairs (x, y) of two adjacent RoPE pairs turned by f = (c0, c1, s0, s1), as
-// hi parts and negated lo parts.
+// fp16 hi parts and negated lo parts.
 __device__ __forceinline__ void rot_split_neg(uint32_t xw, uint32_t yw, const float4& f, uint32_t& xh, uint32_t& xl,
                                               uint32_t& yh, uint32_t& yl) {
   const uint64_t x = bf16x2_to_f2(xw), y = bf16x2_to_f2(yw);
   const uint64_t c = f2_pack(f.x, f.y), sn = f2_pack(f.z, f.w);
-  split_neg_bf16(f2_sub(f2_mul(x, c), f2_mul(y, sn)), xh, xl);
-  split_neg_bf16(f2_fma(x, sn, f2_mul(y, c)), yh, yl);
+  split_neg_f16(f2_sub(f2_mul(x, c), f2_mul(y, sn)), xh, xl);
+  split_neg_f16(f2_fma(x, sn, f2_mul(y, c)), yh, yl);
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  jl::mma_f16(d, a[0], a[1], a[2], a[3], b0, b1);
 }
 
 // B fragments of k-step ks for the unit's 16 keys; tile: the lane's place in the unit's keys.
@@ -172,6 +192,53 @@ __device__ __forceinline__ unsigned atomic_inc_acq_rel(unsigned* p, unsigned las
   unsigned old;
   asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(last) : "memory");
   return old;
+}
+
+// The larger of two values; a NaN stays.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Scores, times scale, of a unit's first n keys, at positions j0 on, as remote pairs, in
+// fp32 throughout: the path of operands outside fp16's range (128K keys all beyond it: 560
+// instead of 99 us).  q: the KV head's r queries; keys: the unit's tile.  Lane l multiplies
+// pairs 2 l and 2 l + 1.
+template <int D>
+__device__ __forceinline__ void plain_scores(float (&x)[2][2], uint32_t keys, const __nv_bfloat16* q, int r, int hq,
+                                             int j0, int n, int G, int dq, uint64_t turn0, uint64_t turn1,
+                                             float scale) {
+  const int lane = threadIdx.x & 31, c4 = lane & 3;
+  const bool mine = 2 * lane < D / 2;
+  const int t = mine ? 2 * lane : 0;
+#pragma unroll 1
+  for (int u = 0; u < n; ++u) {
+    const int j = j0 + u;
+    float s0, c0, s1, c1;
+    sincos_phase(dq - (j / G - j), turn0, &s0, &c0);
+    sincos_phase(dq - (j / G - j), turn1, &s1, &c1);
+    const uint32_t row = keys + u * 128, swz = (u & 7) << 4;
+    uint32_t kx, ky;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(kx) : "r"(row + ((t * 2) ^ swz)));
+    constexpr int kHalf = D == 128 ? 2048 : 0;  // the second coordinates: the next block, or the row's second half
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(ky) : "r"(row + kHalf + ((t * 2 + (D == 128 ? 0 : 64)) ^ swz)));
+    const float x0 = bf16lo_to_f32(kx), x1 = bf16hi_to_f32(kx), y0 = bf16lo_to_f32(ky), y1 = bf16hi_to_f32(ky);
+    // R(dk - dq) k
+    const float a0 = x0 * c0 + y0 * s0, b0 = y0 * c0 - x0 * s0, a1 = x1 * c1 + y1 * s1, b1 = y1 * c1 - x1 * s1;
+#pragma unroll 1
+    for (int h = 0; h < r; ++h) {
+      const uint32_t qx = *reinterpret_cast<const uint32_t*>(q + h * D + t);
+      const uint32_t qy = *reinterpret_cast<const uint32_t*>(q + h * D + D / 2 + t);
+      float v = (bf16lo_to_f32(qx) * a0 + bf16lo_to_f32(qy) * b0) + (bf16hi_to_f32(qx) * a1 + bf16hi_to_f32(qy) * b1);
+      if (!mine) v = 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (hq == h && u == 8 * (i >> 1) + 2 * c4 + (i & 1)) x[i >> 1][i & 1] = v * scale;
+    }
+  }
 }
 
 // A partial result: 8 maxima (log2 units), 8 sums, [r][D] outputs.
@@ -244,7 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float4 f;
     sincos_phase(-e, turn0, &f.z, &f.x);
     sincos_phase(-e, turn1, &f.w, &f.y);
-    *reinterpret_cast<float4*>(smem + C::kEOff + e * C::kERow + qt * 8) = f;
+    *reinterpret_cast<float4*>(smem + C::kEOff + e * C::kERow + qt * 8) =
+        make_float4(f.x * kKeyScale, f.y * kKeyScale, f.z * kKeyScale, f.w * kKeyScale);
   }
 
   // ---- how much there is to do, and where this CTA's and this warp's share is
@@ -588,7 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         sincos_phase(dq - (qd - j0), turn0, &f.z, &f.x);
         sincos_phase(dq - (qd - j0), turn1, &f.w, &f.y);
         __syncwarp();
-        *reinterpret_cast<float4*>(smem + C::kCsOff + warp * D * 4 + qt * 8) = f;  // (D = 64: twice the same)
+        *reinterpret_cast<float4*>(smem + C::kCsOff + warp * D * 4 + qt * 8) =  // (D = 64: twice the same)
+            make_float4(f.x * kQueryScale, f.y * kQueryScale, f.z * kQueryScale, f.w * kQueryScale);
         __syncwarp();
         // packed heads sit in two lanes each: either turns every other k-step
 #pragma unroll
@@ -623,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     h_next = 2 * k;
     if (!wait()) break;
     const uint32_t kst = ring + slot * C::kSlot + tile_off;
+    const bool tail = j0 + 16 > L;
     float x[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
     if (j0 >= 0) {
       // This lane's scores: keys 8 nt + 2 c4 + {0, 1} of head hq.  A unit on the
@@ -652,14 +722,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
             if (kp == 0) {
-              mma_bf16_first(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
-              mma_bf16_first(sal[nt], alo, kal[2 * nt], kal[2 * nt + 1]);
+              mma_f16_first(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
+              mma_f16_first(sal[nt], alo, kal[2 * nt], kal[2 * nt + 1]);
             } else {
-              mma_bf16(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
-              mma_bf16(sal[nt], alo, kal[2 * nt], kal[2 * nt + 1]);
+              mma_f16(sah[nt], alo, kah[2 * nt], kah[2 * nt + 1]);
+              mma_f16(sal[nt], alo, kal[2 * nt], kal[2 * nt + 1]);
             }
-            mma_bf16(sah[nt], ahi, kbh[2 * nt], kbh[2 * nt + 1]);
-            mma_bf16(sal[nt], ahi, kbl[2 * nt], kbl[2 * nt + 1]);
+            mma_f16(sah[nt], ahi, kbh[2 * nt], kbh[2 * nt + 1]);
+            mma_f16(sal[nt], ahi, kbl[2 * nt], kbl[2 * nt + 1]);
           }
         }
 #pragma unroll
@@ -686,28 +756,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (!any_remote || j0 + 8 * nt + 2 * c4 + e >= local_from) x[nt][e] = sb[nt][e];
+            x[nt][e] = !any_remote || j0 + 8 * nt + 2 * c4 + e >= local_from ? sb[nt][e] : x[nt][e] * kUnscale;
       }
-    }
-    pass_on(2 * k);
-    h_next = 2 * k + 1;
-    if (!wait()) break;
-    if (j0 >= 0) {
-      const uint32_t vst = ring + slot * C::kSlot + tile_off;
       // log2 units, the mask behind the sequence, and the running maximum of the lane's head
-      const bool tail = j0 + 16 > L;
+      const float unit_scale = any_local ? sl2 : sl2 * kUnscale;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          x[nt][e] *= sl2;
+          x[nt][e] *= unit_scale;
           if (tail && j0 + 8 * nt + 2 * c4 + e >= L) x[nt][e] = -INFINITY;
         }
-      float mt = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-      const bool grow = mt > m_used + 8.f;  // a maximum up to 2^8 behind keeps every p below 2^8
-      if (__any_sync(0xffffffffu, grow)) {
+      float mt = max_nan(max_nan(x[0][0], x[0][1]), max_nan(x[1][0], x[1][1]));
+      mt = max_nan(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+      mt = max_nan(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+      // a maximum up to 2^8 behind keeps every p below 2^8
+      if (__any_sync(0xffffffffu, !(mt <= m_used + 8.f))) {
+        if (__any_sync(0xffffffffu, mt != mt)) {
+          // An operand beyond fp16's range has infinite hi and lo parts, whose products'
+          // difference is NaN: such remote units, and those of NaN inputs, are scored in fp32.
+          if (any_remote) {
+            const int b = item / a.Hkv;
+            plain_scores<D>(x, ring + slot * C::kSlot, a.q + ((int64_t)b * a.Hq + (item - b * a.Hkv) * r) * D, r, hq,
+                            j0, min(16, min(local_from, L) - j0), G, dq, turn0, turn1, sl2);
+          }
+          mt = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+        }
+        const bool grow = mt > m_used + 8.f;
         const float alpha = grow ? ex2_approx(m_used - mt) : 1.f;  // 0 for the first keys
         l_part *= alpha;
         if (grow) m_used = mt;
@@ -722,6 +799,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           oacc[n][3] *= a1;
         }
       }
+    }
+    pass_on(2 * k);
+    h_next = 2 * k + 1;
+    if (!wait()) break;
+    if (j0 >= 0) {
+      const uint32_t vst = ring + slot * C::kSlot + tile_off;
       const float msub = (m_used == -INFINITY) ? 0.f : m_used;
       uint32_t ph[2], pl[2];  // P^T fragments are the lane's own scores
 #pragma unroll

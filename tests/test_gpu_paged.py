@@ -284,6 +284,27 @@ def test_decode_with_outlier_keys_and_one_dominant_key():
     _check_decode(o, lse, q, k, v, table, lens, 100, 1000, 1e6)
 
 
+@pytest.mark.parametrize("qs,ks,share", [(1e-4, 1e4, 1.0), (1e4, 1e-4, 1.0), (1e-2, 2000.0, 0.02), (5e-3, 800.0, 1.0),
+                                         (3000.0, 1e-3, 1.0), (1e-9, 1e9, 0.3), (1e-30, 1e30, 1.0)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 1, 128), (10, 2, 64)])
+def test_decode_operands_beyond_half_range(qs, ks, share, Hq, Hkv, D):
+    # queries and keys whose products are ordinary and whose own sizes are not: entries above
+    # fp16's range in all keys, in some keys of a unit, in the queries, and just below it.  (The
+    # smaller side of those that stay in range is above 1e-3, where the bound of 2^-17 holds.)
+    g = torch.Generator().manual_seed(int(share * 100) + D)
+    lens, P = [1003, 517, 16], 32
+    k, v = _pool(g, 60, P, Hkv, D)
+    table = _table(g, lens, P, 60)
+    k[torch.rand(60, P, generator=g).to(DEV) < share] *= ks
+    _stale(k, v, table, lens, float("nan"))
+    q = _randn(g, 3, Hq, D) * qs
+    o, lse = torch.empty_like(q), torch.empty(3, Hq, device=DEV)
+    for w0 in (0, 45):  # 45: units on the band's edge
+        jl.jl_bifocal_decode_paged(q, k, v, table, _i32(lens), o, lse, w0=w0, w_pretrained=150, rope_base=1e4,
+                                   workspace=_ws(Hq, Hkv, D))
+        _check_decode(o, lse, q, k, v, table, lens, w0, 150, 1e4)
+
+
 @pytest.mark.parametrize("B,Hq,Hkv,D,top,P", [(300, 4, 2, 64, 60, 16), (300, 2, 2, 128, 400, 32), (40, 24, 3, 64, 130, 16),
                                               (700, 1, 1, 64, 17, 16), (97, 32, 8, 128, 300, 48)])
 def test_decode_many_short_sequences(B, Hq, Hkv, D, top, P):
