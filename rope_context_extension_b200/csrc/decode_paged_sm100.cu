@@ -26,18 +26,17 @@
 // ticket (no spinning), each time in unit order, so results do not depend on
 // timing.
 //
-// Scores use mma.sync m16n8k16 with the query heads on the M axis.  A remote unit
-// that starts at position j0 has dk(j) = dk(j0) - e(j) with e(j) in [0, 15]: the
-// queries take R(dq - dk(j0)), whose D/2 factors the warp's lanes form once per
-// unit, and the keys take R(-e) from a 16-row table, in registers.  Corrected
+// Scores use mma.sync m16n8k16 with the query heads on the M axis.  Remote units from
+// position jb on have dk(j) = dk(jb) - e(j): the queries take R(dq - dk(jb)), formed by
+// the warp's lanes and kept in shared memory while e(j) stays in [0, 31] (one unit or
+// more), and the keys take R(-e) from a 32-row table, in registers.  Corrected
 // operands enter the products as fp16 hi + lo pairs (about 22 significant bits; bf16
 // pairs, 17 bits, put an error of 1.6e-6 on the log-sum of rows that one large key
 // dominates), the queries' lo parts in the M rows 8-15 that at most eight heads leave
 // free.  Keys or queries beyond fp16's range are found by their scores and scored again
-// in fp32.  Probabilities are carried as hi + lo
-// pairs too (2^-17; one bf16 would double the output's own rounding error): for up
-// to four heads, duplicated in M rows 4-7, the lo parts use the columns 4-7 of the
-// P V product, which would be idle.
+// in fp32.  Probabilities are carried as bf16 hi + lo pairs (2^-17; one bf16 would double
+// the output's own rounding error): for up to four heads, duplicated in M rows 4-7, the
+// lo parts use the columns 4-7 of the P V product, which would be idle.
 //
 // Measured (B200, 32 query and 8 KV heads, D 128, w0 4096, G 4; replayed graphs):
 // one sequence of 131072 keys 98-99 us = 5.4 TB/s, 0.83 of a copy; eight of them
