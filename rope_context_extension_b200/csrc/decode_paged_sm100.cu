@@ -46,6 +46,8 @@
 // 57% busy, with the keys' turn and split the most of it.  64 sequences of up to 8192
 // keys (16 heads): 166 us, 0.90.  A sparse step of eight sequences, 97 pages of 64 keys
 // per KV head: 50 us.  777 keys of one D = 64 head: 12.4 us, all latency.
+#include <climits>
+
 #include "jl_mma.cuh"
 #include "jl_paged.cuh"
 
@@ -62,6 +64,11 @@ constexpr int kMinUnits = kWarps;  // units per CTA below which fewer CTAs share
 // two per CTA (measured: 512 items of 7 units 27.5 -> 22.6 us, 8 items of 8 units 16.4
 // -> 21.0 us).
 constexpr int kWholeUnits = 4, kWholeUnitsMany = 8;
+// CTAs take whole items where no CTA then has over three units per warp more than an even
+// share: each unit takes a warp about 1.3 us when little else runs, the CTAs' join 3 to 4
+// us (8 items of 19 units 13.0 -> 10.1 us, of 32 units 13.2 -> 11.6, of 49 units 13.3 ->
+// 14.1; 128 items of 256 units 56 -> 51).
+constexpr int kCtaMore = 3 * kWarps;
 constexpr int kMaxR = 8;
 // Turned operands are scaled by powers of two on their way to fp16: an entry of a key (a
 // query) is off by at most 2^-22 of itself or 2^-31 (2^-29), whichever is more, up to
@@ -86,7 +93,7 @@ struct PgCfg {
   static constexpr int kBarOff = kScanOff + (kSegs + 1) * 8 + 8;
   static constexpr int kMetaOff = (kBarOff + kWarps * kSlots * 8 + 15) / 16 * 16;  // units: item, position, index
   static constexpr int kMiscOff = kMetaOff + kWarps * kMeta * 16;
-  static constexpr int kEntOff = kMiscOff + 16;    // the warps' partials: items, first units, sizes
+  static constexpr int kEntOff = kMiscOff + 16 + kSegs / 32 * 16 + 32;    // the warps' partials: items, first units, sizes
   static constexpr int kSmem = kEntOff + 32 * kWarps + 1024;
   static constexpr int kMaxParts = 160;            // parts that one join weighs: the grid's bound
   static constexpr int kChunk = 8;                 // parts that one thread adds up in one go
@@ -291,6 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n;      // its units
     int item;   // -1: no partial
   };
+  int64_t* run_sums = reinterpret_cast<int64_t*>(smem + C::kMiscOff + 16);  // units that each of the scan's warps counts,
+  int2* run_ends = reinterpret_cast<int2*>(run_sums + kSegs / 32);         // of its items the least and the most
+  int64_t* span = reinterpret_cast<int64_t*>(run_ends + kSegs / 32);       // CTAs at work, this one's stretch of the line
   Entry* ent = reinterpret_cast<Entry*>(smem + C::kEntOff);  // the warps' heads (2 w) and tails (2 w + 1)
 
   // ---- what needs no memory: barriers, key factors
@@ -316,16 +326,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- how much there is to do, and where this CTA's and this warp's share is
   const int per_seg = (items + kSegs - 1) / kSegs;
-  bool any_empty, any_large;
+  int least = INT_MAX, most = 0;  // units of an item
   {
     int64_t v = 0;
-    bool none = false, large = false;
-    const int whole_units = items >= 2 * (int)gridDim.x ? kWholeUnitsMany : kWholeUnits;
     if (tid < kSegs) {
       for (int i = tid * per_seg; i < items && i < (tid + 1) * per_seg; ++i) {
         const int n = item_units(a, i);
-        none = none || n == 0;
-        large = large || n > whole_units;
+        least = min(least, n);
+        most = max(most, n);
         v += n;
       }
 #pragma unroll
@@ -333,18 +341,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += t;
       }
-      scan[tid + 1] = v;
+      least = __reduce_min_sync(0xffffffffu, least);
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 31) {
+        run_sums[warp] = v;
+        run_ends[warp] = make_int2(least, most);
+      }
     }
-    any_empty = __syncthreads_or(none);
-    any_large = __syncthreads_or(large);
-    int64_t before = 0;
-    if (tid < kSegs)
-      for (int w = 0; w < warp; ++w) before += scan[32 * w + 32];
     __syncthreads();
+    int64_t before = 0;
+#pragma unroll
+    for (int w = 0; w < kSegs / 32; ++w) {
+      if (w < warp) before += run_sums[w];
+      least = min(least, run_ends[w].x);
+      most = max(most, run_ends[w].y);
+    }
     if (tid < kSegs) scan[tid + 1] = v + before;
     __syncthreads();
   }
-  const int64_t U = scan[kSegs];
+  const bool any_empty = least == 0;
+  const bool any_large = most > (items >= 2 * (int)gridDim.x ? kWholeUnitsMany : kWholeUnits);
 
   // Sequences and lists with nothing in them, bad lengths and counts: spread over every CTA.
   for (int it = any_empty ? blockIdx.x : items; it < items; it += gridDim.x) {
@@ -360,35 +376,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  // CTAs that share the line, the CTA's stretch of it and the warp's.  Where every item
-  // is small (a batch of short sequences) warps take whole items instead, each counting
-  // its units from 0: a join costs more than the few units that this leaves uneven.
-  int64_t N, c0 = 0, c1 = 0, wb = 0, we = 0;
+  // CTAs that share the line, the CTA's stretch of it and the warp's.  Where that leaves
+  // little uneven, CTAs take an item each, and warps whole items where every item is small
+  // (a batch of short sequences), counting their units from 0, and need no join.
+  int64_t wb, we;
   int first_item = 0;
-  if (any_large) {
-    const int64_t want = (U + kMinUnits - 1) / kMinUnits;
-    N = want < gridDim.x ? want : gridDim.x;
+  bool on_line = false;
+  const int64_t all_units = scan[kSegs];
+  if (any_large && items <= (int)gridDim.x && (int64_t)(most - kCtaMore) * gridDim.x <= all_units) {
+    if (blockIdx.x >= items) return;
+    first_item = blockIdx.x;
+    const int n = item_units(a, first_item);
+    wb = warp * n / kWarps;
+    we = (warp + 1) * n / kWarps;
+    if (tid == 0) span[0] = items, span[1] = 0, span[2] = n;
+  } else if (any_large) {
+    const int64_t want = (all_units + kMinUnits - 1) / kMinUnits;
+    const int64_t N = want < gridDim.x ? want : gridDim.x;
     if (blockIdx.x >= N) return;
-    c0 = div_units((int64_t)blockIdx.x * U, N);
-    c1 = div_units(((int64_t)blockIdx.x + 1) * U, N);
+    const int64_t c0 = div_units((int64_t)blockIdx.x * all_units, N);
+    const int64_t c1 = div_units(((int64_t)blockIdx.x + 1) * all_units, N);
     wb = c0 + warp * (c1 - c0) / kWarps;
     we = c0 + (warp + 1) * (c1 - c0) / kWarps;
+    if (tid == 0) span[0] = N, span[1] = c0, span[2] = c1;
+    on_line = true;
   } else {
-    N = min((items + kWarps - 1) / kWarps, (int)gridDim.x);
-    if (blockIdx.x >= N || U == 0) return;
+    const int64_t N = min((items + kWarps - 1) / kWarps, (int)gridDim.x);
+    if (blockIdx.x >= N || all_units == 0) return;
     const int64_t w = (int64_t)blockIdx.x * kWarps + warp, all = N * kWarps;
     first_item = (int)(w * items / all);
     const int last_item = (int)((w + 1) * items / all);
     int n = 0;
     for (int i = first_item + lane; i < last_item; i += 32) n += item_units(a, i);
+    wb = 0;
     we = __reduce_add_sync(0xffffffffu, n);
+    if (tid == 0) span[0] = N, span[1] = 0, span[2] = 0;
   }
-  const int cnt = (int)(we - wb);
+  const int cnt = (int)(we - wb);  // (below, wb + cnt: one value less through the walk)
 
   // ---- the walk over units: lane l holds the description of unit 32 * batch + l
   int cur_it = first_item;
   int64_t cur_s = 0;  // cur_it: an item at or before the batch's first unit; cur_s: its first unit
-  if (cnt > 0 && any_large) {
+  if (cnt > 0 && on_line) {
     // the run of items that holds unit wb, found by all lanes together
     int seg = 0;
     for (int t0 = 0; t0 < kSegs; t0 += 32) {
@@ -597,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool began = seg_k >= seg_c;
         const int64_t first = wb + seg_k - seg_c;
         const int n = k == cnt || !began ? item_units(a, item) : 0;
-        const bool ends = k < cnt || first + n <= we;
+        const bool ends = k < cnt || first + n <= wb + cnt;
         if (began && ends) {
           store_final(item);
         } else if (k < cnt) {  // begun before this warp's range
@@ -870,6 +899,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // A part's weight 2^(m - M): an empty part's sum is 0, and a NaN that left the maximum at -inf goes through.
   auto weight = [](float m, float l, float M) { return m == -INFINITY ? l : ex2_approx(m - M); };
+  // (kept in shared memory meanwhile: in registers they cost the walk 2%)
+  const int64_t U = scan[kSegs], N = span[0], c0 = span[1], c1 = span[2];
   static_assert(2 * kWarps <= 32 && kWarps < 16 && D >= 64, "entries in lanes; a part per lane of half a warp");
   // lane e holds entry e: heads at 2 w, tails at 2 w + 1
   const int my_item = lane < 2 * kWarps ? ent[lane].item : -1;
