@@ -39,13 +39,13 @@
 // lo parts use the columns 4-7 of the P V product, which would be idle.
 //
 // Measured (B200, 32 query and 8 KV heads, D 128, w0 4096, G 4; replayed graphs):
-// one sequence of 131072 keys 98-99 us = 5.4 TB/s, 0.83 of a copy; eight of them
+// one sequence of 131072 keys 97-98 us = 5.5 TB/s, 0.84 of a copy; eight of them
 // 665-755 us = 5.7-6.5 TB/s by the clock that the power limit leaves (1.0003 bytes of
 // DRAM per byte needed).  The fixed part is about 16 us: 4.5 us to the first keys,
 // 1.5 us for the warps' join, 6 us for tickets and the CTAs' join; the issue slots are
 // 57% busy, with the keys' turn and split the most of it.  64 sequences of up to 8192
 // keys (16 heads): 166 us, 0.90.  A sparse step of eight sequences, 97 pages of 64 keys
-// per KV head: 50 us.  777 keys of one D = 64 head: 12.4 us, all latency.
+// per KV head: 50 us.  777 keys of one D = 64 head: 12.5 us, all latency.
 #include <climits>
 
 #include "jl_mma.cuh"
