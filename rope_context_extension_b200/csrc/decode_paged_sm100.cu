@@ -93,7 +93,7 @@ struct PgCfg {
   static constexpr int kBarOff = kScanOff + (kSegs + 1) * 8 + 8;
   static constexpr int kMetaOff = (kBarOff + kWarps * kSlots * 8 + 15) / 16 * 16;  // units: item, position, index
   static constexpr int kMiscOff = kMetaOff + kWarps * kMeta * 16;
-  static constexpr int kEntOff = kMiscOff + 16 + kSegs / 32 * 16 + 32;    // the warps' partials: items, first units, sizes
+  static constexpr int kEntOff = kMiscOff + 16 + kSegs / 32 * 16 + 32;  // the warps' partials: items, units
   static constexpr int kSmem = kEntOff + 32 * kWarps + 1024;
   static constexpr int kMaxParts = 160;            // parts that one join weighs: the grid's bound
   static constexpr int kChunk = 8;                 // parts that one thread adds up in one go
@@ -298,9 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n;      // its units
     int item;   // -1: no partial
   };
-  int64_t* run_sums = reinterpret_cast<int64_t*>(smem + C::kMiscOff + 16);  // units that each of the scan's warps counts,
-  int2* run_ends = reinterpret_cast<int2*>(run_sums + kSegs / 32);         // of its items the least and the most
-  int64_t* span = reinterpret_cast<int64_t*>(run_ends + kSegs / 32);       // CTAs at work, this one's stretch of the line
+  // units that each of the scan's warps counts, of its items the least and the most; the
+  // CTAs at work and this one's stretch of the line
+  int64_t* run_sums = reinterpret_cast<int64_t*>(smem + C::kMiscOff + 16);
+  int2* run_ends = reinterpret_cast<int2*>(run_sums + kSegs / 32);
+  int64_t* span = reinterpret_cast<int64_t*>(run_ends + kSegs / 32);
   Entry* ent = reinterpret_cast<Entry*>(smem + C::kEntOff);  // the warps' heads (2 w) and tails (2 w + 1)
 
   // ---- what needs no memory: barriers, key factors

@@ -32,7 +32,7 @@ namespace jl {
 namespace {
 
 constexpr int kNrThreads = 256;
-constexpr int kBlocksPerSm = 3;  // resident at 80 registers a thread (a grid of four: 131072 tokens 796 us, not 524)
+constexpr int kBlocksPerSm = 3;  // resident at 80 registers a thread (a grid of four: 131072 tokens 796 us)
 
 // A packed fp32 pair rounded to bf16x2.
 __device__ __forceinline__ uint32_t f2_to_bf16x2(uint64_t v) {
@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kNrThreads, kBlocksPerSm) norm_rope_kernel(con
         if (w != nullptr) {
           const float inv = rsqrtf(ss * (1.f / D) + a.eps);
           const uint64_t inv2 = f2_pack(inv, inv);
-          const uint4 wl = *reinterpret_cast<const uint4*>(w + 8 * sub), wh = *reinterpret_cast<const uint4*>(w + H2 + 8 * sub);
+          const uint4 wl = *reinterpret_cast<const uint4*>(w + 8 * sub);
+          const uint4 wh = *reinterpret_cast<const uint4*>(w + H2 + 8 * sub);
           const uint32_t wx[4] = {wl.x, wl.y, wl.z, wl.w}, wy[4] = {wh.x, wh.y, wh.z, wh.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -210,7 +211,8 @@ cudaError_t launch_d(NormRopeArgs& a, cudaStream_t stream) {
     }
   }
   const int64_t tasks = (int64_t)a.T * a.tasks_per_token;
-  const int64_t blocks = std::min<int64_t>((tasks + kNrThreads / 32 - 1) / (kNrThreads / 32), (int64_t)sms * kBlocksPerSm);
+  const int64_t blocks =
+      std::min<int64_t>((tasks + kNrThreads / 32 - 1) / (kNrThreads / 32), (int64_t)sms * kBlocksPerSm);
   norm_rope_kernel<D><<<(unsigned)blocks, kNrThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
